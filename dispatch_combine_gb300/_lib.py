@@ -22,6 +22,16 @@ MOE_SCORE_SIGMOID_BIAS = 0
 MOE_SCORE_SOFTMAX = 1
 MOE_LAYOUT_CONTIGUOUS = 0
 MOE_LAYOUT_MASKED = 1
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP16 = 1
+MOE_NORM_RMS = 0
+MOE_NORM_LAYER = 1
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_FULL = 3
+MOE_ROPE_HALF = 0
+MOE_ROPE_PAIRS = 1
 
 STATUS_NAMES = {
     0: "MOE_OK",
@@ -48,7 +58,25 @@ class MoeShape(ctypes.Structure):
                 ("score", ctypes.c_int32), ("bias_scale", ctypes.c_float)]
 
 
+class MoeNorm(ctypes.Structure):
+    """Mirror of moe_norm_t."""
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
+class MoeKv(ctypes.Structure):
+    """Mirror of moe_kv_t."""
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 _PS = ctypes.POINTER(MoeShape)
+_PN = ctypes.POINTER(MoeNorm)
+_PK = ctypes.POINTER(MoeKv)
+_I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_I32]),
     "moe_workspace_size": (_I32, [_PS, ctypes.POINTER(_SZ)]),
@@ -87,6 +115,15 @@ SIGNATURES = {
     "moe_router_prep_size": (_I32, [_PS, ctypes.POINTER(_SZ)]),
     "moe_router_prepare": (_I32, [_PS, _P, _P, _SZ, _P]),
     "moe_router_release": (_I32, [_P]),
+    "moe_norm_in": (_I32, [_PN, _P, _I64, _P, _P, _P, _I64, _P]),
+    "moe_norm_out": (_I32, [_PN, _P, _I64, _P, _I64, _I32, _P, _P, _I32, _P, _I64, _F32, _P, _P,
+                            _P, _I64, _P, _I64, _P]),
+    "moe_kv_append": (_I32, [_PK, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _I32, _P,
+                             _P, _P, _I64, _P, _SZ, _P]),
+    "moe_prefix_attention_workspace_size": (_I32, [_PK, _I32, _I32, _I32, _I32,
+                                                   ctypes.POINTER(_SZ)]),
+    "moe_prefix_attention": (_I32, [_PK, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _P, _I32, _P,
+                                    _I32, _P, _F32, _P, _I64, _P, _P, _SZ, _P]),
     "moe_selftest_wait_timeout": (_I32, [_P, _SZ, _U64, _P]),
 }
 
@@ -633,6 +670,207 @@ def moe_layer_fp8(shape, x, w_r, bias, w_gu_q, w_gu_s, w_dn_q, w_dn_s, ws: Works
                                _ptr(w_gu_s), _ptr(w_dn_q), _ptr(w_dn_s), _ptr(y), _ptr(counts),
                                ws.c_ptr, ws.nbytes, _stream(stream)))
     return y
+
+
+# --------------------------------------------------------------------------
+# the rest of the block: norms, cache append, shared-prefix attention
+# --------------------------------------------------------------------------
+
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16}
+
+
+def _dtype(t):
+    if t not in _DTYPES:
+        raise TypeError(f"expected torch.bfloat16 or torch.float16, got {t}")
+    return _DTYPES[t]
+
+
+def _rows(t, dtype, shape, name):
+    """Pointer and row stride of a tensor whose rows (its first dimension) may
+    be strided, each row dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    _expect(t, dtype, shape, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor must be on a CUDA device")
+    width = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != width:
+            raise ValueError(f"{name}: each row must be dense")
+        width *= n
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if t.shape[0] > 1 else width)
+
+
+def _vec(t, dtype, n, name):
+    if t is not None:
+        _expect(t, dtype, (n,), name)
+    return _ptr(t)
+
+
+def moe_norm_in(x, weight=None, bias=None, kind=MOE_NORM_RMS, eps=1e-6, weight_offset=0.0,
+                out=None, stream=None):
+    """out = N(x) * (weight + weight_offset) + bias over the rows of x [T,d]."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [T, d]")
+    T, d = x.shape
+    n = MoeNorm(T, d, int(kind), _dtype(x.dtype), float(eps), float(weight_offset))
+    if out is None:
+        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    xp, xs = _rows(x, x.dtype, (T, d), "x")
+    op, os_ = _rows(out, x.dtype, (T, d), "out")
+    _check("moe_norm_in",
+           lib().moe_norm_in(ctypes.byref(n), xp, xs, _vec(weight, x.dtype, d, "weight"),
+                             _vec(bias, x.dtype, d, "bias"), op, os_, _stream(stream)))
+    return out
+
+
+def moe_norm_out(f, x, post_weight=None, post_bias=None, gate=None, residual_scale=1.0,
+                 next_weight=None, next_bias=None, kind=MOE_NORM_RMS, eps=1e-6,
+                 weight_offset=0.0, post_norm=None, next_norm=None, x_out=None, next_out=None,
+                 stream=None):
+    """Block output f [T,d] into the residual stream x [T,d], and the norm in
+    front of the next block (see moe_norm_out in moe.h).  gate: [d], [T],
+    [T,1] or [T,d] (a [T] gate where T == d is passed as [T,1]).  post_norm /
+    next_norm default to whether a weight (next: or next_out) is given.
+    Returns (x_out, next_out or None)."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [T, d]")
+    T, d = x.shape
+    dt = x.dtype
+    n = MoeNorm(T, d, int(kind), _dtype(dt), float(eps), float(weight_offset))
+    if post_norm is None:
+        post_norm = post_weight is not None
+    if next_norm is None:
+        next_norm = next_weight is not None or next_out is not None
+    gate_kind, gp, gs = MOE_GATE_NONE, None, 0
+    if gate is not None:
+        if gate.dim() == 2 and tuple(gate.shape) == (T, d) and d > 1:
+            gate_kind = MOE_GATE_FULL
+            gp, gs = _rows(gate, dt, (T, d), "gate")
+        elif gate.dim() == 1 and gate.shape[0] == d:
+            gate_kind, gp = MOE_GATE_CHANNEL, _vec(gate, dt, d, "gate")
+        else:
+            if tuple(gate.shape) not in ((T,), (T, 1)):
+                raise ValueError(f"gate: expected [{d}], [{T}], [{T}, 1] or [{T}, {d}], got "
+                                 f"{tuple(gate.shape)}")
+            gate_kind, gp = MOE_GATE_TOKEN, _vec(gate.reshape(-1), dt, T, "gate")
+    if x_out is None:
+        x_out = torch.empty((T, d), dtype=dt, device=x.device)
+    np_, ns = None, 0
+    if next_norm:
+        if next_out is None:
+            next_out = torch.empty((T, d), dtype=dt, device=x.device)
+        np_, ns = _rows(next_out, dt, (T, d), "next_out")
+    fp, fs = _rows(f, dt, (T, d), "f")
+    xp, xs = _rows(x, dt, (T, d), "x")
+    xo, xos = _rows(x_out, dt, (T, d), "x_out")
+    _check("moe_norm_out",
+           lib().moe_norm_out(ctypes.byref(n), fp, fs, xp, xs, int(bool(post_norm)),
+                              _vec(post_weight, dt, d, "post_weight"),
+                              _vec(post_bias, dt, d, "post_bias"), gate_kind, gp, gs,
+                              float(residual_scale), _vec(next_weight, dt, d, "next_weight"),
+                              _vec(next_bias, dt, d, "next_bias"), xo, xos, np_, ns,
+                              _stream(stream)))
+    return x_out, next_out if next_norm else None
+
+
+def kv_struct(num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+              dtype=torch.bfloat16) -> MoeKv:
+    return MoeKv(int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size),
+                 int(num_pages), _dtype(dtype) if isinstance(dtype, torch.dtype) else int(dtype))
+
+
+def _kv_dtype(kv):
+    return torch.bfloat16 if kv.dtype == MOE_DTYPE_BF16 else torch.float16
+
+
+def _caches(kv, k_cache, v_cache):
+    shape = (kv.num_pages, kv.num_kv_heads, kv.page_size, kv.head_dim)
+    _expect(k_cache, _kv_dtype(kv), shape, "k_cache")
+    _expect(v_cache, _kv_dtype(kv), shape, "v_cache")
+    return _ptr(k_cache), _ptr(v_cache)
+
+
+def moe_kv_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cache,
+                  ws: Workspace = None, style=MOE_ROPE_HALF, q_out=None, stream=None):
+    """Rotate q [T, Hq, D] (returned, or None when q is None) and k [T, Hkv,
+    D] by their positions and append k and v to the cache at `slots`.  The
+    first 2 * len(inv_freq) elements of each head turn (inv_freq None: none)."""
+    dt = _kv_dtype(kv)
+    T = k.shape[0]
+    qp, qs, qo, qos = None, 0, None, 0
+    if q is not None:
+        qp, qs = _rows(q, dt, (T, kv.num_q_heads, kv.head_dim), "q")
+        if q_out is None:
+            q_out = torch.empty((T, kv.num_q_heads, kv.head_dim), dtype=dt, device=q.device)
+        qo, qos = _rows(q_out, dt, (T, kv.num_q_heads, kv.head_dim), "q_out")
+    kp, ks = _rows(k, dt, (T, kv.num_kv_heads, kv.head_dim), "k")
+    vp, vs = _rows(v, dt, (T, kv.num_kv_heads, kv.head_dim), "v")
+    rot = 0
+    if inv_freq is not None:
+        _expect(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq")
+        _expect(positions, torch.int32, (T,), "positions")
+        rot = 2 * inv_freq.numel()
+    _expect(slots, torch.int32, (T,), "slots")
+    kc, vc = _caches(kv, k_cache, v_cache)
+    _check("moe_kv_append",
+           lib().moe_kv_append(ctypes.byref(kv), T, qp, qs, kp, ks, vp, vs, _ptr(positions),
+                               _ptr(slots), _ptr(inv_freq), rot, int(style), kc, vc, qo, qos,
+                               ws.c_ptr if ws is not None else None,
+                               ws.nbytes if ws is not None else 0, _stream(stream)))
+    return q_out if q is not None else None
+
+
+def moe_prefix_attention_workspace_size(kv: MoeKv, T: int, num_seqs: int, max_q: int,
+                                        prefix_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_prefix_attention_workspace_size",
+           lib().moe_prefix_attention_workspace_size(ctypes.byref(kv), int(T), int(num_seqs),
+                                                     int(max_q), int(prefix_len),
+                                                     ctypes.byref(out)))
+    return out.value
+
+
+def moe_prefix_attention(kv: MoeKv, q, k_cache, v_cache, prefix_pages, prefix_len: int,
+                         page_table, kv_lens, ws: Workspace, q_offsets=None, max_q: int = 1,
+                         scale=None, out=None, lse=None, want_lse=False, stream=None):
+    """Attention of q [T, Hq, D] over a shared prefix and each sequence's own
+    rows (see moe_prefix_attention in moe.h; scale defaults to D ** -0.5).
+    Returns (out, lse or None)."""
+    dt = _kv_dtype(kv)
+    T, B = q.shape[0], kv_lens.shape[0]
+    if out is None:
+        out = torch.empty((T, kv.num_q_heads, kv.head_dim), dtype=dt, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((T, kv.num_q_heads), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _expect(lse, torch.float32, (T, kv.num_q_heads), "lse")
+    qp, qs = _rows(q, dt, (T, kv.num_q_heads, kv.head_dim), "q")
+    op, os_ = _rows(out, dt, (T, kv.num_q_heads, kv.head_dim), "out")
+    kc, vc = _caches(kv, k_cache, v_cache)
+    _expect(kv_lens, torch.int32, (B,), "kv_lens")
+    max_pages = 0
+    if page_table is not None:
+        max_pages = page_table.shape[1]
+        _expect(page_table, torch.int32, (B, max_pages), "page_table")
+    if q_offsets is not None:
+        _expect(q_offsets, torch.int32, (B + 1,), "q_offsets")
+    if prefix_len > 0:
+        if prefix_pages is None:
+            raise ValueError("prefix_pages: missing")
+        if prefix_pages.dtype != torch.int32:
+            raise TypeError("prefix_pages: expected torch.int32")
+        if prefix_pages.numel() * kv.page_size < prefix_len:
+            raise ValueError("prefix_pages: fewer pages than prefix_len needs")
+    _check("moe_prefix_attention",
+           lib().moe_prefix_attention(ctypes.byref(kv), T, B, int(max_q), qp, qs,
+                                      _ptr(q_offsets), kc, vc,
+                                      _ptr(prefix_pages) if prefix_len > 0 else None,
+                                      int(prefix_len), _ptr(page_table), max_pages,
+                                      _ptr(kv_lens),
+                                      float(kv.head_dim ** -0.5 if scale is None else scale),
+                                      op, os_, _ptr(lse), ws.c_ptr, ws.nbytes, _stream(stream)))
+    return out, lse
 
 
 def moe_selftest_wait_timeout(ws: Workspace, limit_ns: int, stream=None):

@@ -215,6 +215,52 @@ cudaError_t launch_wait_selftest(uint32_t *status, uint64_t limit_ns, cudaStream
 
 int num_sms();
 
+// norm.cu
+// One row pass of moe_norm_in / moe_norm_out (strides in elements).
+struct NormArgs {
+  const void *f;     // block output rows (moe_norm_in: the input rows)
+  const void *x;     // residual rows (nullptr: moe_norm_in)
+  const void *pw, *pb;  // post norm weight and bias
+  const void *gate;
+  const void *nw, *nb;  // next norm weight and bias
+  void *x_out, *n_out;
+  int64_t f_stride, x_stride, gate_stride, x_out_stride, n_out_stride;
+  int T, d;
+  int kind, post, gate_kind;
+  float eps, w_off, residual_scale;
+};
+cudaError_t launch_norm(const NormArgs &a, int dtype, cudaStream_t s);
+
+// kv_append.cu
+struct KvAppendArgs {
+  const void *q, *k, *v;
+  const int32_t *positions, *slots;
+  const float *inv_freq;
+  void *k_cache, *v_cache, *q_out;
+  uint32_t *status;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int T, hq, hkv, D, page_shift, rot, style;
+  int64_t num_slots;
+};
+cudaError_t launch_kv_append(const KvAppendArgs &a, int dtype, cudaStream_t s);
+
+// prefix_attention.cu
+struct PrefixAttnArgs {
+  const void *q, *k_cache, *v_cache;
+  const int32_t *q_offsets, *prefix_pages, *page_table, *kv_lens;
+  void *o;
+  float *lse;
+  uint32_t *status;
+  int64_t q_stride, o_stride;
+  int T, B, max_q, hq, hkv, D, page_shift, num_pages, prefix_len, max_pages;
+  float scale;
+  uint8_t *scratch;  // prefix_attention_scratch_bytes
+  uint64_t wait_limit_ns;  // 0: kDefaultWaitLimitNs
+};
+size_t prefix_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D,
+                                      int prefix_len);
+cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, int dtype, cudaStream_t s);
+
 // api.cu: the shape validation every entry point applies (MOE_OK or an error)
 moe_status_t check_shape_for_abi(const moe_shape_t *shape);
 

@@ -458,6 +458,159 @@ moe_status_t moe_eplb_plan(const double *load, int32_t num_experts, int32_t num_
                            int32_t num_nodes, int32_t num_gpus, int32_t num_physical,
                            int32_t *gpu_slots, int32_t *replicas);
 
+/* ------------------------------------------------------------------------
+ * The rest of the decoder block around the layer: norms before and after a
+ * block, the append to a paged key/value cache, and the attention that reads
+ * it for a batch that shares a long prefix.  Forward only, like the layer.
+ * ------------------------------------------------------------------------ */
+
+/* Element type of activations, weights and caches of these calls. */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1 } moe_dtype_t;
+
+typedef enum {
+  MOE_NORM_RMS = 0,  /* v / sqrt(mean(v^2) + eps) */
+  MOE_NORM_LAYER = 1 /* (v - mean) / sqrt(mean((v - mean)^2) + eps) */
+} moe_norm_kind_t;
+
+/* What the gate of moe_norm_out is: absent, one value per channel [d], per
+ * token [T], or per token and channel [T,d]. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1,
+  MOE_GATE_TOKEN = 2,
+  MOE_GATE_FULL = 3
+} moe_gate_t;
+
+/* T rows of d values; every row tensor has its own row stride in elements.
+ * Limits (MOE_ERR_INVALID_ARG beyond them): T >= 0, d % 8 == 0, 8 <= d <=
+ * 16384, eps >= 0 and finite, strides >= d and multiples of 8. */
+typedef struct {
+  int32_t T;
+  int32_t d;
+  int32_t kind;  /* moe_norm_kind_t */
+  int32_t dtype; /* moe_dtype_t, of every tensor of the call */
+  float eps;
+  float weight_offset; /* added to the norm weights: 0, or 1 for weights stored around zero */
+} moe_norm_t;
+
+/*
+ * The norm in front of a block: out = N(x) * (weight + weight_offset) + bias,
+ * N the statistic of `kind` over each row.
+ *   x, out [T,d] with row strides x_stride / out_stride; weight [d] (NULL: 1),
+ *   bias [d] (NULL: 0).  Statistics and arithmetic in fp32, one rounding at
+ *   the end.  out may be x (same stride).
+ */
+moe_status_t moe_norm_in(const moe_norm_t *norm, const void *x, int64_t x_stride,
+                         const void *weight, const void *bias, void *out, int64_t out_stride,
+                         moe_stream_t stream);
+
+/*
+ * Everything between a block's output and the next block's input, in one
+ * pass over the rows:
+ *   v     = post norm ? N(f) * (post_weight + weight_offset) + post_bias : f
+ *   r     = residual_scale * x + gate * v
+ *   x_out = r rounded once
+ *   next_out = N(r) * (next_weight + weight_offset) + next_bias
+ *   post_norm != 0 selects the post norm (post_weight NULL: 1, post_bias
+ *   NULL: 0); gate [d], [T] or [T,d] by gate_kind (a moe_gate_t; gate_stride
+ *   is the row stride of the [T,d] form); next_out NULL skips the second
+ *   norm (next_weight NULL: 1, next_bias NULL: 0).  The second norm is taken
+ *   of r as it stands in fp32, not of the rounded x_out.
+ *   x_out may be x, and next_out may be f (same strides).
+ */
+moe_status_t moe_norm_out(const moe_norm_t *norm, const void *f, int64_t f_stride, const void *x,
+                          int64_t x_stride, int32_t post_norm, const void *post_weight,
+                          const void *post_bias, int32_t gate_kind, const void *gate,
+                          int64_t gate_stride, float residual_scale, const void *next_weight,
+                          const void *next_bias, void *x_out, int64_t x_out_stride,
+                          void *next_out, int64_t next_out_stride, moe_stream_t stream);
+
+/* Heads and paged cache of one attention layer.
+ * k_cache and v_cache are each [num_pages, num_kv_heads, page_size, head_dim]:
+ * the rows of one head in one page are contiguous.
+ * Limits: num_q_heads a multiple of num_kv_heads with at most 128 query heads
+ * per key head, head_dim 64 or 128, page_size a power of two from 16 to 256
+ * (MOE_ERR_UNSUPPORTED otherwise); num_pages * num_kv_heads * page_size <
+ * 2^31 rows (the cache itself may pass 2^32 elements). */
+typedef struct {
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t dtype; /* moe_dtype_t */
+} moe_kv_t;
+
+/* Which elements of a head are rotated together: i and i + rot_dim/2, or
+ * 2i and 2i + 1. */
+typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_PAIRS = 1 } moe_rope_t;
+
+/*
+ * Append T tokens to the cache, with the position rotation on the way.
+ *   q [T, num_q_heads, head_dim], k and v [T, num_kv_heads, head_dim] with
+ *   token strides in elements (heads of a token are contiguous), so that all
+ *   three may be slices of one projection's output;
+ *   positions [T] int32 (rotation angle of pair i: position * inv_freq[i]);
+ *   slots [T] int32: page * page_size + row of the token, -1 for a token that
+ *   is not appended (its q_out is still written);
+ *   inv_freq [rot_dim/2] fp32; the first rot_dim elements of each head turn
+ *   (rot_dim % 16 == 0, 0 <= rot_dim <= head_dim), the rest is copied;
+ *   q_out [T, num_q_heads, head_dim] with its token stride; may be q (same
+ *   stride); q NULL: keys and values only.
+ * The angle is reduced in fp64 (exact to 1e-7 turns up to 2^31 positions),
+ * sine, cosine and the rotation are fp32, one rounding at the end.
+ * A slot outside [-1, num_pages * page_size) is skipped and reported as
+ * MOE_ERR_INVALID_ARG in the workspace's status word (ws of at least 256
+ * bytes; NULL: not reported).  Slots must be distinct: of two tokens with one
+ * slot, either may win.
+ * Pointers 16-byte aligned, strides multiples of 8.
+ */
+moe_status_t moe_kv_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t q_stride,
+                           const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           const int32_t *positions, const int32_t *slots, const float *inv_freq,
+                           int32_t rot_dim, int32_t style, void *k_cache, void *v_cache,
+                           void *q_out, int64_t q_out_stride, void *ws, size_t ws_bytes,
+                           moe_stream_t stream);
+
+/*
+ * Attention of a batch whose sequences share a prefix: the prefix's keys and
+ * values are read once for all of them, then each sequence's own.
+ *   q [T, num_q_heads, head_dim] with token stride q_stride: the new tokens
+ *   of num_seqs sequences, sequence b holding tokens [q_offsets[b],
+ *   q_offsets[b+1]) (int32 [num_seqs+1], device; NULL: one token each, T ==
+ *   num_seqs), at most max_q of them;
+ *   prefix_pages int32 (device): the pages of the shared prefix in order,
+ *   ceil(prefix_len / page_size) of them (prefix_len on the host, 0: none);
+ *   page_table [num_seqs, max_pages] int32 (device): each sequence's own
+ *   pages, which follow the prefix; kv_lens [num_seqs] int32 (device): rows
+ *   of its own in the cache, the new tokens included.
+ *   Token i of the n new ones of a sequence sees the whole prefix and its
+ *   sequence's own rows j < kv_lens - n + i + 1.
+ *   o [T, num_q_heads, head_dim] with token stride o_stride; lse [T,
+ *   num_q_heads] fp32 (NULL to skip): ln of the row's sum of exponentials.
+ *   A token that sees nothing gets zeros and -inf.
+ *   scores are scale * q.k (scale > 0, finite); softmax statistics and sums are fp32, the
+ *   probabilities are rounded to the cache's type for the product with V.
+ * What lies in pages past kv_lens or past the prefix's end is never used,
+ * whatever it holds; the rows below kv_lens must be finite.
+ * Errors on the device: a page id outside [0, num_pages), kv_lens negative or
+ * beyond max_pages * page_size, or q_offsets that decrease, leave [0, T] or
+ * give a sequence more than max_q tokens set MOE_ERR_INVALID_ARG; the values
+ * are clamped, the affected rows undefined and nothing outside the buffers is
+ * touched.
+ * num_seqs <= 4096 (MOE_ERR_UNSUPPORTED beyond).
+ */
+moe_status_t moe_prefix_attention_workspace_size(const moe_kv_t *kv, int32_t T, int32_t num_seqs,
+                                                 int32_t max_q, int32_t prefix_len,
+                                                 size_t *bytes);
+moe_status_t moe_prefix_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, int32_t max_q,
+                                  const void *q, int64_t q_stride, const int32_t *q_offsets,
+                                  const void *k_cache, const void *v_cache,
+                                  const int32_t *prefix_pages, int32_t prefix_len,
+                                  const int32_t *page_table, int32_t max_pages,
+                                  const int32_t *kv_lens, float scale, void *o, int64_t o_stride,
+                                  float *lse, void *ws, size_t ws_bytes, moe_stream_t stream);
+
 /*
  * Number of kernels moe_layer launches per call for this shape (for launch
  * accounting).
