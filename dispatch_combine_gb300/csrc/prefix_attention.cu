@@ -189,6 +189,14 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *m
       : "memory");
 }
 
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -213,6 +221,17 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// mbar_wait_bounded with its clock read put off: reading the global timer takes
+// about a microsecond, longer than most waits here, so a wait first tries for
+// as long as several tiles take.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                         uint32_t *status, uint64_t limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 1024; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity, abort, status, limit_ns);
 }
 
 // Time-bounded wait that ignores the abort flag (to drain after an abort).
@@ -375,7 +394,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     auto segment = [&](bool own, int head, int tok0, int ntok, int lim0, int kv_len, int t0, int t1,
                        int wide, int64_t slot, const int32_t *pages) {
       const uint32_t r = nseg % kDescs;
-      ok = mbar_wait_bounded(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status,
+      ok = wait_bar(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status,
                              limit);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
@@ -386,7 +405,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       ++nseg;
       for (int h = q0; h < q0 + 1 + wide; ++h) {
-        ok = mbar_wait_bounded(&bar.q_empty[h], (q_use[h] & 1u) ^ 1u, abort_flag, a.status, limit);
+        ok = wait_bar(&bar.q_empty[h], (q_use[h] & 1u) ^ 1u, abort_flag, a.status, limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         ++q_use[h];
@@ -424,7 +443,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           uint64_t *full = which ? &bar.v_full[stage] : &bar.k_full[stage];
-          ok = mbar_wait_bounded(which ? &bar.v_empty[stage] : &bar.k_empty[stage], par, abort_flag,
+          ok = wait_bar(which ? &bar.v_empty[stage] : &bar.k_empty[stage], par, abort_flag,
                                  a.status, limit);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) return;
@@ -511,7 +530,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (ok) {  // the end
       const uint32_t r = nseg % kDescs;
-      ok = mbar_wait_bounded(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status,
+      ok = wait_bar(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status,
                              limit);
       if (ok && lane == 0) {
         bar.seg[r] = Segment{0, 0, 0, 0, 0, 0, 0, 0};
@@ -532,87 +551,91 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (q_use[h]) wait_drain(&bar.q_full[h], (q_use[h] - 1) & 1u, limit);
   } else if (warp == 9) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t kIdescQK = attn_idesc<DTYPE>(128, kTile, false);
-      constexpr uint32_t kIdescPV = attn_idesc<DTYPE>(128, D, true);
-      uint32_t kc = 0, vc = 0, nseg = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
-      bool ok = true, any = false;
-      while (ok) {
-        const uint32_t r = nseg % kDescs;
-        if (!mbar_wait_bounded(&bar.d_full[r], (nseg / kDescs) & 1u, abort_flag, a.status, limit))
-          break;
-        const int tiles = bar.seg[r].t1 - bar.seg[r].t0, wide = bar.seg[r].wide;
-        mbar_arrive(&bar.d_empty[r]);
-        if (tiles == 0) break;
-        const int steps = tiles << wide;
-        const int q0 = wide ? 0 : nseg & 1;
-        ++nseg;
-        // scores of step s (group s & 1)
-        auto scores = [&](int s) {
-          const int w = s & 1;
-          if (s < 1 + wide) {  // the first use of a query buffer
-            const int h = q0 + s;
-            if (!mbar_wait_bounded(&bar.q_full[h], q_use[h] & 1u, abort_flag, a.status, limit))
-              return false;
-            ++q_use[h];
-          }
-          const int stage = kc % C::STAGES;
-          if (!wide || w == 0) {
-            if (!mbar_wait_bounded(&bar.k_full[stage], (kc / C::STAGES) & 1u, abort_flag, a.status,
-                                   limit))
-              return false;
-          }
-          tc_fence_after();
-          const uint32_t qa = smem_u32(smem + (wide ? w : q0) * C::TILE_BYTES);
-          const uint32_t ka = smem_u32(smem + C::K_OFF + stage * C::TILE_BYTES);
+    // The whole warp walks the steps and one elected lane issues: the values
+    // then stay warp-uniform, and a 128 x 128 x 16 product takes the tensor
+    // cores only 64 cycles, less than a divergent lane needs to form its
+    // operands.
+    constexpr uint32_t kIdescQK = attn_idesc<DTYPE>(128, kTile, false);
+    constexpr uint32_t kIdescPV = attn_idesc<DTYPE>(128, D, true);
+    const uint64_t desc_q = sw128_kmajor_desc(smem_u32(smem));
+    const uint64_t desc_k = sw128_kmajor_desc(smem_u32(smem + C::K_OFF));
+    const uint64_t desc_v = sw128_nmajor_desc(smem_u32(smem + C::V_OFF), C::BLK);
+    uint32_t kc = 0, vc = 0, nseg = 0;
+    uint32_t q_par = 0, p_par = 0;  // a bit per buffer / group
+    bool ok = true, any = false;
+    auto wait = [&](uint64_t *b, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, wait_bar(b, parity, abort_flag, a.status, limit));
+      return ok;
+    };
+    while (ok) {
+      const uint32_t r = nseg % kDescs;
+      if (!wait(&bar.d_full[r], (nseg / kDescs) & 1u)) break;
+      const int tiles = __reduce_max_sync(0xffffffffu, bar.seg[r].t1 - bar.seg[r].t0);
+      const int wide = __reduce_max_sync(0xffffffffu, bar.seg[r].wide);
+      if (lane == 0) mbar_arrive(&bar.d_empty[r]);
+      if (tiles == 0) break;
+      const int steps = tiles << wide;
+      const int q0 = wide ? 0 : nseg & 1;
+      ++nseg;
+      // scores of step s (group s & 1)
+      auto scores = [&](int s) {
+        const int w = s & 1;
+        if (s < 1 + wide) {  // the first use of a query buffer
+          const int h = q0 + s;
+          if (!wait(&bar.q_full[h], (q_par >> h) & 1u)) return;
+          q_par ^= 1u << h;
+        }
+        const uint32_t stage = kc % C::STAGES;
+        if (!wide || w == 0) {
+          if (!wait(&bar.k_full[stage], (kc / C::STAGES) & 1u)) return;
+        }
+        tc_fence_after();
+        const uint64_t qd = desc_q + static_cast<uint32_t>((wide ? w : q0) * (C::TILE_BYTES / 16));
+        const uint64_t kd = desc_k + stage * (C::TILE_BYTES / 16);
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_bf16_ss(tmem_base + w * 128,
-                        sw128_kmajor_desc(qa + (k / 4) * C::BLK) + 2u * (k & 3),
-                        sw128_kmajor_desc(ka + (k / 4) * C::BLK) + 2u * (k & 3), kIdescQK,
-                        k ? 1u : 0u);
-          any = true;
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = (k / 4) * (C::BLK / 16) + 2 * (k & 3);
+            mma_bf16_ss(tmem_base + w * 128, qd + at, kd + at, kIdescQK, k ? 1u : 0u);
+          }
           mma_commit(&bar.s_full[w]);
-          if (!wide || w == 1) {
-            mma_commit(&bar.k_empty[stage]);
-            ++kc;
-          }
+          if (!wide || w == 1) mma_commit(&bar.k_empty[stage]);
           if (wide ? s >= steps - 2 : s == steps - 1) mma_commit(&bar.q_empty[wide ? w : q0]);
-          return true;
-        };
-        ok = scores(0) && (steps < 2 || scores(1));
-        for (int s = 0; ok && s < steps; ++s) {
-          const int w = s & 1;
-          const int stage = vc % C::STAGES;
-          if (!mbar_wait_bounded(&bar.p_full[w], p_use[w] & 1u, abort_flag, a.status, limit) ||
-              ((!wide || w == 0) &&
-               !mbar_wait_bounded(&bar.v_full[stage], (vc / C::STAGES) & 1u, abort_flag, a.status,
-                                  limit))) {
-            ok = false;
-            break;
-          }
-          ++p_use[w];
-          tc_fence_after();
-          const uint32_t va = smem_u32(smem + C::V_OFF + stage * C::TILE_BYTES);
+        }
+        __syncwarp();
+        any = true;
+        if (!wide || w == 1) ++kc;
+      };
+      scores(0);
+      if (ok && steps > 1) scores(1);
+      for (int s = 0; ok && s < steps; ++s) {
+        const int w = s & 1;
+        const uint32_t stage = vc % C::STAGES;
+        if (!wide || w == 0) {
+          if (!wait(&bar.v_full[stage], (vc / C::STAGES) & 1u)) break;
+        }
+        if (!wait(&bar.p_full[w], (p_par >> w) & 1u)) break;
+        p_par ^= 1u << w;
+        tc_fence_after();
+        const uint64_t vd = desc_v + stage * (C::TILE_BYTES / 16);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem_base + 256 + w * 128, tmem_base + w * 128 + k * 8,
-                   sw128_nmajor_desc(va + k * 16 * 128, C::BLK), kIdescPV,
-                   (s >= 2 || k) ? 1u : 0u);
-          if (!wide || w == 1) {
-            mma_commit(&bar.v_empty[stage]);
-            ++vc;
-          }
+            mma_ts(tmem_base + 256 + w * 128, tmem_base + w * 128 + k * 8, vd + k * (16 * 128 / 16),
+                   kIdescPV, (s >= 2 || k) ? 1u : 0u);
+          if (!wide || w == 1) mma_commit(&bar.v_empty[stage]);
           if (s >= steps - 2) mma_commit(&bar.o_full[w]);
-          if (s + 2 < steps) ok = scores(s + 2);
         }
-      }
-      if (any) {
-        mma_commit(&bar.drain);
-        wait_drain(&bar.drain, 0, limit);
+        __syncwarp();
+        if (!wide || w == 1) ++vc;
+        if (s + 2 < steps) scores(s + 2);
       }
     }
-    __syncwarp();
+    if (any) {
+      if (elect_one()) mma_commit(&bar.drain);
+      __syncwarp();
+      wait_drain(&bar.drain, 0, limit);
+    }
   } else {
     // ---------------- softmax: group w = warps 4w .. 4w+3, a row per thread ----------------
     const int w = warp >> 2, quad = warp & 3;
@@ -632,7 +655,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     while (ok) {
       const uint32_t r = nseg % kDescs;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar.d_full[r], (nseg / kDescs) & 1u,
+      ok = __all_sync(0xffffffffu, wait_bar(&bar.d_full[r], (nseg / kDescs) & 1u,
                                                      abort_flag, a.status, limit));
       if (!ok) break;
       const Segment sg = bar.seg[r];
@@ -651,7 +674,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int i = 0; i < steps; ++i) {
         const int ti = sg.wide ? i : 2 * i + w;  // tile of the segment
         const int t = sg.t0 + ti;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar.s_full[w], s_use & 1u, abort_flag,
+        ok = __all_sync(0xffffffffu, wait_bar(&bar.s_full[w], s_use & 1u, abort_flag,
                                                        a.status, limit));
         if (!ok) break;
         ++s_use;
@@ -671,14 +694,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               for (int j = 0; j < 32; ++j)
                 if (c * 32 + j >= vis) v[c][j] = 0xff800000u;  // -inf
           }
-          float top = -INFINITY;
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int j = 0; j < 32; j += 2)
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
+            for (int c = 0; c < 4; ++c) {
               const float x = __uint_as_float(v[c][j]), y = __uint_as_float(v[c][j + 1]);
-              asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(x), "f"(y));
+              asm("max.f32 %0, %0, %1, %2;" : "+f"(tops[c]) : "f"(x), "f"(y));
             }
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
           const bool moves = top > m + lag;
           if (__any_sync(0xffffffffu, moves)) {
             const float m1 = moves ? top : m;
@@ -702,6 +726,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           const float c0 = m == -INFINITY ? kOff : kOff - m * sl2;
           const uint64_t c0x2 = pack_f32x2(c0, c0);
+          uint64_t sums[4] = {l2, 0, 0, 0};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t p[16];
@@ -713,11 +738,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               float2 e = unpack_f32x2(x);
               e.x = ex2(e.x);
               e.y = ex2(e.y);
-              l2 = add_f32x2(l2, pack_f32x2(e.x, e.y));
+              sums[j & 3] = add_f32x2(sums[j & 3], pack_f32x2(e.x, e.y));
               p[j] = pack2<DTYPE>(e.x, e.y);
             }
             tmem_st_32x32b_x16(ts + c * 16, p);
           }
+          l2 = add_f32x2(add_f32x2(sums[0], sums[1]), add_f32x2(sums[2], sums[3]));
           tmem_st_wait();
         }
         // rows of V past the keys' end may hold anything, and 0 * NaN is not
@@ -726,7 +752,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (valid < kTile && (!sg.wide || w == 0)) {
           const uint32_t at = vc + ti;
           ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bar.v_full[at % C::STAGES], (at / C::STAGES) & 1u,
+                          wait_bar(&bar.v_full[at % C::STAGES], (at / C::STAGES) & 1u,
                                             abort_flag, a.status, limit));
           if (!ok) break;
           if (row >= valid) {
@@ -752,7 +778,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (mine) g.part_lse[at] = -INFINITY;
         continue;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar.o_full[w], o_use & 1u, abort_flag,
+      ok = __all_sync(0xffffffffu, wait_bar(&bar.o_full[w], o_use & 1u, abort_flag,
                                                      a.status, limit));
       if (!ok) break;
       ++o_use;
@@ -791,7 +817,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// joining the parts: one CTA per token, a warp per query head at a time
+// joining the parts: a warp per token and query head
 // ---------------------------------------------------------------------------
 
 template <int DTYPE, int D>
@@ -825,7 +851,8 @@ __global__ void __launch_bounds__(256) prefix_attention_join_kernel(const AttnAr
     cum = m.cum;
     unit = m.unit;
   }
-  for (int h = threadIdx.x >> 5; h < a.hq; h += blockDim.x >> 5) {
+  const int h = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (h < a.hq) {
     const int kvh = h / g.G, hg = h - kvh * g.G;
     // parts: `n` of them `step` rows apart from row `first`, of two kinds
     int64_t first[2] = {0, 0};
@@ -1014,8 +1041,9 @@ cudaError_t run(const PrefixAttnArgs &a, cudaStream_t s) {
                    C::SMEM_BYTES, s, tmK, tmV, tmQp, tmQs, g);
   }
   const int warps = std::min(8, a.hq);
-  MOE_LAUNCH_PDL(prefix_attention_join_kernel<DTYPE, D>, static_cast<unsigned>(a.T), warps * 32, 0,
-                 s, g, planned);
+  MOE_LAUNCH_PDL(prefix_attention_join_kernel<DTYPE, D>,
+                 dim3(static_cast<unsigned>(a.T), (a.hq + warps - 1) / warps), warps * 32, 0, s, g,
+                 planned);
   return cudaGetLastError();
 }
 
