@@ -20,7 +20,9 @@
 // A CTA's two groups of 128 softmax threads each own a 128 x 128 score tile
 // and an output accumulator in TMEM.  A wide unit (more than 128 rows) gives
 // each group 128 of its rows and both read the same K and V tiles; a narrow
-// one gives both the same rows and every second tile.
+// one gives both the same rows and every second tile.  The groups take turns
+// through all segments, so while one ends a short unit the other is at the
+// next.
 //
 // Bounds: with many rows the tensor cores (4 D flop per score; the two MMAs
 // of one group run while the other group takes exponentials), with few the
@@ -69,10 +71,6 @@ struct SeqMeta {
   int32_t unit;  // number of its first unit among the own units
   int32_t tiles;
 };
-struct PlanHeader {
-  int64_t total;
-  int32_t pieces;
-};
 
 struct AttnArgs {
   PrefixAttnArgs a;
@@ -81,7 +79,7 @@ struct AttnArgs {
   int s_wide, s_tok, s_rows, s_box;
   int64_t p_cost, p_total;    // of a prefix unit, of all
   int64_t s_slot0;            // first row of the own units' slots
-  PlanHeader *head;
+  int64_t *piece;  // the length of a piece
   SeqMeta *meta;
   float *part_o, *part_lse;
 };
@@ -122,17 +120,16 @@ __device__ __forceinline__ Seq read_seq(const AttnArgs &g, int b, bool *bad_off,
   return s;
 }
 
-// pieces of the line: each at least as long as the longest tile
-__device__ __forceinline__ int pieces_of(int64_t total, int ctas) {
-  const int64_t most = total / kWideCost;
-  return static_cast<int>(most < 1 ? 1 : most < ctas ? most : ctas);
+// The line is cut into pieces of one length, at least the longest tile's.
+// 64-bit divisions are kept out of line: they are long code.
+__device__ __noinline__ int64_t div64(int64_t n, int64_t d) { return n / d; }
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if (n < (int64_t{1} << 31) && d < (int64_t{1} << 31))
+    return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+  return div64(n, d);
 }
-__device__ __forceinline__ int64_t piece_start(int64_t total, int pieces, int c) {
-  return total * c / pieces;
-}
-// the piece that holds position pos: the largest c with piece_start(c) <= pos
-__device__ __forceinline__ int piece_of(int64_t total, int pieces, int64_t pos) {
-  return static_cast<int>(((pos + 1) * pieces - 1) / total);
+__device__ __forceinline__ int64_t piece_length(int64_t total, int ctas) {
+  return max(quotient(total + ctas - 1, ctas), static_cast<int64_t>(kWideCost));
 }
 
 // ---------------------------------------------------------------------------
@@ -223,19 +220,34 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// mbar_wait_bounded with its clock read put off: reading the global timer takes
-// about a microsecond, longer than most waits here, so a wait first tries for
-// as long as several tiles take.
+// whether the phase with this parity is complete, without waiting
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The bounded wait, out of line: its code is long, and it reads the global
+// timer, which takes about a microsecond.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                       uint32_t *status, uint64_t limit_ns) {
+  return mbar_wait_bounded(bar, parity, abort, status, limit_ns);
+}
+// Whole warp: true for all lanes when the phase completed, false for all when
+// some lane gave up.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort,
                                          uint32_t *status, uint64_t limit_ns) {
 #pragma unroll 1
-  for (int i = 0; i < 1024; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_bounded(bar, parity, abort, status, limit_ns);
+  for (int i = 0; i < 256; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_long(bar, parity, abort, status, limit_ns));
 }
-
 // Time-bounded wait that ignores the abort flag (to drain after an abort).
-__device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+__device__ __noinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -254,7 +266,7 @@ struct Bars {
   uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2];  // scores of a group are in TMEM
-  uint64_t p_full[2];  // its probabilities are
+  uint64_t p_lo[2], p_hi[2];  // its probabilities are: keys 0-63, 64-127
   uint64_t o_full[2];  // its segment's accumulator is complete
   uint64_t d_full[kDescs], d_empty[kDescs];
   uint64_t drain;
@@ -328,7 +340,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&bar.q_full[h], 1);
       mbar_init(&bar.q_empty[h], 1);
       mbar_init(&bar.s_full[h], 1);
-      mbar_init(&bar.p_full[h], 4);
+      mbar_init(&bar.p_lo[h], 4);
+      mbar_init(&bar.p_hi[h], 4);
       mbar_init(&bar.o_full[h], 1);
     }
     for (int i = 0; i < kDescs; ++i) {
@@ -353,10 +366,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   units_before += units - my_units;
   if (drop) own_total = 0;
   const int64_t total = g.p_total + own_total;
-  const int pieces = pieces_of(total, gridDim.x);
-  const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= pieces;
-  const int64_t lo = idle ? 0 : piece_start(total, pieces, blockIdx.x);
-  const int64_t hi = idle ? 0 : piece_start(total, pieces, blockIdx.x + 1);
+  const int64_t piece = piece_length(total, gridDim.x);
+  const int64_t lo = blockIdx.x * piece, hi = min(lo + piece, total);
+  const bool idle = lo >= total;
   if (blockIdx.x == 0 || !idle) {
     const int64_t from = max(lo - g.p_total, int64_t{0});
     int64_t cum = before;
@@ -374,7 +386,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (blockIdx.x == 0) {
       if (bad || bad_off) set_status(a.status, kStatusBadId);
-      if (threadIdx.x == 0) *g.head = PlanHeader{total, pieces};
+      if (threadIdx.x == 0) *g.piece = piece;
     }
   }
   if (idle) return;  // uniform across the CTA
@@ -388,26 +400,117 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ---------------- loader: walks the line, fetches Q, K and V ----------------
     const int ppt = max(1, kTile >> a.page_shift);  // pages per tile
     const int page_rows = min(1 << a.page_shift, kTile);
-    uint32_t issued[2] = {0, 0}, nseg = 0, q_use[2] = {0, 0};  // K and V tiles
+    uint32_t issued[2] = {0, 0}, nseg = 0, q_use[2] = {0, 0};  // issued: K and V tiles
     bool ok = true;
-    // one segment: publish it, then fetch its tiles
-    auto segment = [&](bool own, int head, int tok0, int ntok, int lim0, int kv_len, int t0, int t1,
-                       int wide, int64_t slot, const int32_t *pages) {
+    // tiles [t0, t1) of a unit that starts at `start` in the line with n tiles
+    // of the given width; false: none of them here
+    int t0, t1;
+    auto tile_at = [&](int64_t ahead, int n, int wide) {  // first tile at or past `ahead`
+      if (ahead <= 0) return 0;
+      if (ahead >= static_cast<int64_t>(n) * (wide ? kWideCost : kNarrowCost)) return n;
+      const int x = static_cast<int>(ahead);
+      return wide ? (x + kWideCost - 1) / kWideCost : (x + kNarrowCost - 1) / kNarrowCost;
+    };
+    auto cut = [&](int64_t start, int n, int wide) {
+      t0 = tile_at(lo - start, n, wide);
+      t1 = tile_at(hi - start, n, wide);
+      return t0 < t1;
+    };
+    // the prefix units of this piece, then its sequences, 32 at a time (one
+    // per lane; `todo`: those with work here), each with its units
+    int64_t u = lo < g.p_total ? quotient(lo, g.p_cost) : 0;
+    bool own = lo >= g.p_total;
+    int base = bar.start_seq - 32, seq = 0;
+    int64_t cum0 = g.p_total + bar.start_cum, cum = 0, start = 0, unit_cost = 1;
+    int unit0 = bar.start_unit, un = 0, batch_units = 0;
+    int64_t batch = 0;
+    unsigned todo = 0;
+    Seq s = {0, 0, 0, 0, 0, 0};
+    int j = 0, n_units = 0, q0 = 0, nq = 0, len = 0, tiles = 0, unit = 0;
+    while (ok) {
+      int head, tok0, ntok, lim0, kv_len, wide;
+      int64_t slot;
+      const int32_t *pages;
+      if (!own) {
+        if (u * g.p_cost >= min(hi, g.p_total)) {
+          own = true;
+          continue;
+        }
+        const int64_t at = u++;
+        if (!cut(at * g.p_cost, g.p_tiles, g.p_wide)) continue;
+        head = static_cast<int>(quotient(at, g.p_blocks));
+        tok0 = static_cast<int>(at - static_cast<int64_t>(head) * g.p_blocks) * g.p_tok;
+        ntok = min(g.p_tok, a.T - tok0);
+        lim0 = kv_len = a.prefix_len;
+        wide = g.p_wide;
+        slot = (at + blockIdx.x) * 2 * g.p_rows;
+        pages = a.prefix_pages;
+      } else if (j < n_units && start + j * unit_cost < hi) {
+        const int at = j++;
+        if (!cut(start + at * unit_cost, tiles, g.s_wide)) continue;
+        const int block = at / a.hkv;
+        head = at - block * a.hkv;
+        const int i0 = block * g.s_tok;
+        tok0 = q0 + i0;
+        ntok = min(g.s_tok, nq - i0);
+        lim0 = len - nq + i0 + 1;
+        kv_len = len;
+        wide = g.s_wide;
+        slot = g.s_slot0 + (static_cast<int64_t>(unit + at) + blockIdx.x) * 2 * g.s_rows;
+        pages = a.page_table + static_cast<int64_t>(seq) * a.max_pages;
+      } else if (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        seq = base + src;
+        q0 = __shfl_sync(0xffffffffu, s.q0, src);
+        nq = __shfl_sync(0xffffffffu, s.nq, src);
+        len = __shfl_sync(0xffffffffu, s.len, src);
+        tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+        n_units = __shfl_sync(0xffffffffu, s.units, src);
+        start = __shfl_sync(0xffffffffu, cum, src);
+        unit = __shfl_sync(0xffffffffu, un, src);
+        unit_cost = static_cast<int64_t>(tiles) * (g.s_wide ? kWideCost : kNarrowCost) + kUnitCost;
+        j = lo <= start ? 0 : static_cast<int>(quotient(lo - start, unit_cost));
+        continue;
+      } else {
+        base += 32;
+        cum0 += batch;
+        unit0 += batch_units;
+        if (base >= a.B || cum0 >= hi) break;
+        s = read_seq(g, base + lane, &bad_off, &bad);
+        cum = s.cost;
+        un = s.units;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t c = __shfl_up_sync(0xffffffffu, cum, off);
+          const int v = __shfl_up_sync(0xffffffffu, un, off);
+          if (lane >= off) {
+            cum += c;
+            un += v;
+          }
+        }
+        batch = __shfl_sync(0xffffffffu, cum, 31);
+        batch_units = __shfl_sync(0xffffffffu, un, 31);
+        cum += cum0 - s.cost;
+        un += unit0 - s.units;
+        todo = __ballot_sync(0xffffffffu, s.cost > 0 && cum < hi && cum + s.cost > lo);
+        continue;
+      }
+      // publish the segment, then fetch its queries and tiles
       const uint32_t r = nseg % kDescs;
-      ok = wait_bar(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status,
-                             limit);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const int q0 = wide ? 0 : nseg & 1;  // a narrow unit's rows alternate between the buffers
+      ok = wait_bar(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status, limit);
+      if (!ok) break;
+      const int h0 = wide ? 0 : nseg & 1;  // a narrow unit's rows alternate between the buffers
       if (lane == 0) {
         bar.seg[r] = Segment{t0, t1, kv_len, wide, ntok, lim0, own ? g.s_rows : g.p_rows, slot};
         mbar_arrive(&bar.d_full[r]);
       }
       ++nseg;
-      for (int h = q0; h < q0 + 1 + wide; ++h) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h < h0 || h > h0 + wide) continue;
         ok = wait_bar(&bar.q_empty[h], (q_use[h] & 1u) ^ 1u, abort_flag, a.status, limit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
+        if (!ok) break;
         ++q_use[h];
         if (lane == 0) {
           const int box = own ? g.s_box : g.p_box;
@@ -417,6 +520,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         d * 64, head * g.G, tok0 + (wide ? h * g.tpt : 0));
         }
       }
+      if (!ok) break;
       auto page_at = [&](int t) {
         int p = -1;
         const int first = static_cast<int>((static_cast<int64_t>(t) * kTile) >> a.page_shift);
@@ -431,6 +535,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         return p;
       };
       int page = page_at(t0);
+#pragma unroll 1
       for (int t = t0; t < t1; ++t) {
         const int next = page_at(t + 1);
         const int stage = issued[0] % C::STAGES;
@@ -444,9 +549,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int which = 0; which < 2; ++which) {
           uint64_t *full = which ? &bar.v_full[stage] : &bar.k_full[stage];
           ok = wait_bar(which ? &bar.v_empty[stage] : &bar.k_empty[stage], par, abort_flag,
-                                 a.status, limit);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) return;
+                        a.status, limit);
+          if (!ok) break;
           ++issued[which];
           if (lane == 0) mbar_arrive_expect_tx(full, bytes);
           __syncwarp();
@@ -458,80 +562,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               tma_load_2d(dst + d * C::BLK, which ? &tmV : &tmK, full, d * 64, row);
           }
         }
+        if (!ok) break;
         page = next;
-      }
-    };
-    // tiles [t0, t1) of a unit that starts at `start` with tiles of cost w
-    auto cut = [&](int64_t start, int n, int w, int *t0, int *t1) {
-      const int64_t f = lo - start, e = hi - start;
-      *t0 = f <= 0 ? 0 : static_cast<int>(min((f + w - 1) / w, static_cast<int64_t>(n)));
-      *t1 = e <= 0 ? 0 : static_cast<int>(min((e + w - 1) / w, static_cast<int64_t>(n)));
-      return *t0 < *t1;
-    };
-    int t0, t1;
-    if (lo < g.p_total) {
-      const int w = g.p_wide ? kWideCost : kNarrowCost;
-      for (int64_t u = lo / g.p_cost; ok && u * g.p_cost < min(hi, g.p_total); ++u) {
-        if (!cut(u * g.p_cost, g.p_tiles, w, &t0, &t1)) continue;
-        const int head = static_cast<int>(u / g.p_blocks);
-        const int tok0 = static_cast<int>(u - static_cast<int64_t>(head) * g.p_blocks) * g.p_tok;
-        segment(false, head, tok0, min(g.p_tok, a.T - tok0), a.prefix_len, a.prefix_len, t0, t1,
-                g.p_wide, (u + blockIdx.x) * 2 * g.p_rows, a.prefix_pages);
-      }
-    }
-    if (hi > g.p_total) {
-      const int w = g.s_wide ? kWideCost : kNarrowCost;
-      int64_t cum0 = g.p_total + bar.start_cum;
-      int unit0 = bar.start_unit;
-      // 32 sequences at a time, one per lane
-      for (int base = bar.start_seq; ok && base < a.B && cum0 < hi; base += 32) {
-        const Seq s = read_seq(g, base + lane, &bad_off, &bad);
-        int64_t cum = s.cost;
-        int un = s.units;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int64_t c = __shfl_up_sync(0xffffffffu, cum, off);
-          const int u = __shfl_up_sync(0xffffffffu, un, off);
-          if (lane >= off) {
-            cum += c;
-            un += u;
-          }
-        }
-        const int64_t batch = __shfl_sync(0xffffffffu, cum, 31);
-        const int batch_units = __shfl_sync(0xffffffffu, un, 31);
-        cum += cum0 - s.cost;
-        un += unit0 - s.units;
-        unsigned todo =
-            __ballot_sync(0xffffffffu, s.cost > 0 && cum < hi && cum + s.cost > lo);
-        while (todo && ok) {
-          const int src = __ffs(todo) - 1;
-          todo &= todo - 1;
-          const int q0 = __shfl_sync(0xffffffffu, s.q0, src), nq = __shfl_sync(0xffffffffu, s.nq, src);
-          const int len = __shfl_sync(0xffffffffu, s.len, src);
-          const int tiles = __shfl_sync(0xffffffffu, s.tiles, src);
-          const int n_units = __shfl_sync(0xffffffffu, s.units, src);
-          const int64_t start = __shfl_sync(0xffffffffu, cum, src);
-          const int unit = __shfl_sync(0xffffffffu, un, src);
-          const int64_t c = static_cast<int64_t>(tiles) * w + kUnitCost;
-          int j = lo <= start ? 0 : static_cast<int>((lo - start) / c);
-          for (; ok && j < n_units && start + j * c < hi; ++j) {
-            if (!cut(start + j * c, tiles, w, &t0, &t1)) continue;
-            const int block = j / a.hkv, head = j - block * a.hkv;
-            const int i0 = block * g.s_tok;
-            segment(true, head, q0 + i0, min(g.s_tok, nq - i0), len - nq + i0 + 1, len, t0, t1,
-                    g.s_wide,
-                    g.s_slot0 + (static_cast<int64_t>(unit + j) + blockIdx.x) * 2 * g.s_rows,
-                    a.page_table + static_cast<int64_t>(base + src) * a.max_pages);
-          }
-        }
-        cum0 += batch;
-        unit0 += batch_units;
       }
     }
     if (ok) {  // the end
       const uint32_t r = nseg % kDescs;
-      ok = wait_bar(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status,
-                             limit);
+      ok = wait_bar(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status, limit);
       if (ok && lane == 0) {
         bar.seg[r] = Segment{0, 0, 0, 0, 0, 0, 0, 0};
         mbar_arrive(&bar.d_full[r]);
@@ -542,96 +579,143 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // is complete when its barrier has passed that use's phase
 #pragma unroll
     for (int which = 0; which < 2; ++which)
-      for (int s = 0; s < C::STAGES; ++s) {
+#pragma unroll 1
+      for (int st = 0; st < C::STAGES; ++st) {
         const uint32_t uses = issued[which] / C::STAGES +
-                              (s < static_cast<int>(issued[which] % C::STAGES) ? 1u : 0u);
-        if (uses) wait_drain(which ? &bar.v_full[s] : &bar.k_full[s], (uses - 1) & 1u, limit);
+                              (st < static_cast<int>(issued[which] % C::STAGES) ? 1u : 0u);
+        if (uses) wait_drain(which ? &bar.v_full[st] : &bar.k_full[st], (uses - 1) & 1u, limit);
       }
+#pragma unroll
     for (int h = 0; h < 2; ++h)
       if (q_use[h]) wait_drain(&bar.q_full[h], (q_use[h] - 1) & 1u, limit);
   } else if (warp == 9) {
     // ---------------- MMA issuer ----------------
-    // The whole warp walks the steps and one elected lane issues: the values
-    // then stay warp-uniform, and a 128 x 128 x 16 product takes the tensor
-    // cores only 64 cycles, less than a divergent lane needs to form its
-    // operands.
+    // Steps are numbered through all segments; step n belongs to group n & 1.
+    // Scores run up to two steps ahead of products with V: scores(n + 2)
+    // overwrite the probabilities of step n, so they follow product(n) (MMAs
+    // complete in issue order).  Issuing takes as long as computing (64 cycles
+    // for 128 x 128 x 16) except for the last four, the depth of the queue in
+    // front of the tensor cores, so what lies between two batches must stay
+    // below 256 cycles.  The whole warp walks the steps, so that operands stay
+    // warp-uniform, and one elected lane issues.
     constexpr uint32_t kIdescQK = attn_idesc<DTYPE>(128, kTile, false);
     constexpr uint32_t kIdescPV = attn_idesc<DTYPE>(128, D, true);
     const uint64_t desc_q = sw128_kmajor_desc(smem_u32(smem));
     const uint64_t desc_k = sw128_kmajor_desc(smem_u32(smem + C::K_OFF));
     const uint64_t desc_v = sw128_nmajor_desc(smem_u32(smem + C::V_OFF), C::BLK);
-    uint32_t kc = 0, vc = 0, nseg = 0;
+    // cursors of the scores and of the products: steps done, segments opened,
+    // tiles done, steps left in the segment, step in the segment, its width
+    uint32_t s_n = 0, s_seg = 0, s_tile = 0, o_n = 0, o_seg = 0, o_tile = 0;
+    int s_left = 0, s_i = 0, s_wide = 0, o_left = 0, o_i = 0, o_wide = 0;
     uint32_t q_par = 0, p_par = 0;  // a bit per buffer / group
-    bool ok = true, any = false;
-    auto wait = [&](uint64_t *b, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, wait_bar(b, parity, abort_flag, a.status, limit));
-      return ok;
-    };
-    while (ok) {
-      const uint32_t r = nseg % kDescs;
-      if (!wait(&bar.d_full[r], (nseg / kDescs) & 1u)) break;
-      const int tiles = __reduce_max_sync(0xffffffffu, bar.seg[r].t1 - bar.seg[r].t0);
-      const int wide = __reduce_max_sync(0xffffffffu, bar.seg[r].wide);
-      if (lane == 0) mbar_arrive(&bar.d_empty[r]);
-      if (tiles == 0) break;
-      const int steps = tiles << wide;
-      const int q0 = wide ? 0 : nseg & 1;
-      ++nseg;
-      // scores of step s (group s & 1)
-      auto scores = [&](int s) {
-        const int w = s & 1;
-        if (s < 1 + wide) {  // the first use of a query buffer
-          const int h = q0 + s;
-          if (!wait(&bar.q_full[h], (q_par >> h) & 1u)) return;
-          q_par ^= 1u << h;
-        }
-        const uint32_t stage = kc % C::STAGES;
-        if (!wide || w == 0) {
-          if (!wait(&bar.k_full[stage], (kc / C::STAGES) & 1u)) return;
-        }
-        tc_fence_after();
-        const uint64_t qd = desc_q + static_cast<uint32_t>((wide ? w : q0) * (C::TILE_BYTES / 16));
-        const uint64_t kd = desc_k + stage * (C::TILE_BYTES / 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = (k / 4) * (C::BLK / 16) + 2 * (k & 3);
-            mma_bf16_ss(tmem_base + w * 128, qd + at, kd + at, kIdescQK, k ? 1u : 0u);
+    bool end = false;
+    auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+    while (true) {
+      // ---- the next scores, if everything is there (or nothing else can be done)
+      if (s_n < o_n + 2 && !end) {
+        const bool alone = s_n == o_n;
+        bool have = s_left > 0;
+        if (!have) {
+          const uint32_t r = s_seg % kDescs, par = (s_seg / kDescs) & 1u;
+          have = all(mbar_test(&bar.d_full[r], par));
+          if (!have && alone) {
+            have = wait_bar(&bar.d_full[r], par, abort_flag, a.status, limit);
+            if (!have) break;
           }
-          mma_commit(&bar.s_full[w]);
-          if (!wide || w == 1) mma_commit(&bar.k_empty[stage]);
-          if (wide ? s >= steps - 2 : s == steps - 1) mma_commit(&bar.q_empty[wide ? w : q0]);
+          if (have) {
+            const int tiles = __reduce_max_sync(0xffffffffu, bar.seg[r].t1 - bar.seg[r].t0);
+            s_wide = __reduce_max_sync(0xffffffffu, bar.seg[r].wide);
+            s_left = tiles << s_wide;
+            s_i = 0;
+            ++s_seg;
+            end = tiles == 0;
+            if (end) continue;
+          }
         }
-        __syncwarp();
-        any = true;
-        if (!wide || w == 1) ++kc;
-      };
-      scores(0);
-      if (ok && steps > 1) scores(1);
-      for (int s = 0; ok && s < steps; ++s) {
-        const int w = s & 1;
-        const uint32_t stage = vc % C::STAGES;
-        if (!wide || w == 0) {
-          if (!wait(&bar.v_full[stage], (vc / C::STAGES) & 1u)) break;
-        }
-        if (!wait(&bar.p_full[w], (p_par >> w) & 1u)) break;
-        p_par ^= 1u << w;
-        tc_fence_after();
-        const uint64_t vd = desc_v + stage * (C::TILE_BYTES / 16);
-        if (elect_one()) {
+        if (have) {
+          const int w = s_n & 1, h = s_wide ? w : (s_seg - 1) & 1;
+          const bool first_q = s_i <= s_wide;
+          const uint32_t stage = s_tile % C::STAGES, k_par = (s_tile / C::STAGES) & 1u;
+          bool there = all(mbar_test(&bar.k_full[stage], k_par) &&
+                           (!first_q || mbar_test(&bar.q_full[h], (q_par >> h) & 1u)));
+          if (!there && alone) {
+            there = wait_bar(&bar.k_full[stage], k_par, abort_flag, a.status, limit) &&
+                    (!first_q ||
+                     wait_bar(&bar.q_full[h], (q_par >> h) & 1u, abort_flag, a.status, limit));
+            if (!there) break;
+          }
+          if (there) {
+            tc_fence_after();
+            const uint64_t qd = desc_q + static_cast<uint32_t>(h * (C::TILE_BYTES / 16));
+            const uint64_t kd = desc_k + stage * (C::TILE_BYTES / 16);
+            const bool last_k = !s_wide || (s_i & 1);
+            if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem_base + 256 + w * 128, tmem_base + w * 128 + k * 8, vd + k * (16 * 128 / 16),
-                   kIdescPV, (s >= 2 || k) ? 1u : 0u);
-          if (!wide || w == 1) mma_commit(&bar.v_empty[stage]);
-          if (s >= steps - 2) mma_commit(&bar.o_full[w]);
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = (k / 4) * (C::BLK / 16) + 2 * (k & 3);
+                mma_bf16_ss(tmem_base + w * 128, qd + at, kd + at, kIdescQK, k ? 1u : 0u);
+              }
+              mma_commit(&bar.s_full[w]);
+              if (last_k) mma_commit(&bar.k_empty[stage]);
+              if (s_left <= 1 + s_wide) mma_commit(&bar.q_empty[h]);
+            }
+            __syncwarp();
+            if (first_q) q_par ^= 1u << h;
+            s_tile += last_k;
+            ++s_i;
+            --s_left;
+            ++s_n;
+            continue;
+          }
         }
-        __syncwarp();
-        if (!wide || w == 1) ++vc;
-        if (s + 2 < steps) scores(s + 2);
       }
+      if (s_n == o_n) break;  // the end
+      // ---- the next product; its first half of keys may be ready early
+      if (o_left == 0) {  // its segment was opened by the scores
+        const uint32_t r = o_seg % kDescs;
+        const int tiles = __reduce_max_sync(0xffffffffu, bar.seg[r].t1 - bar.seg[r].t0);
+        o_wide = __reduce_max_sync(0xffffffffu, bar.seg[r].wide);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.d_empty[r]);
+        o_left = tiles << o_wide;
+        o_i = 0;
+        ++o_seg;
+      }
+      const int w = o_n & 1;
+      const uint32_t stage = o_tile % C::STAGES, v_par = (o_tile / C::STAGES) & 1u;
+      const uint32_t par = (p_par >> w) & 1u;
+      const uint64_t vd = desc_v + stage * (C::TILE_BYTES / 16);
+      const uint32_t t_p = tmem_base + w * 128, t_o = tmem_base + 256 + w * 128;
+      if (!all(mbar_test(&bar.v_full[stage], v_par) && mbar_test(&bar.p_lo[w], par))) {
+        if (!wait_bar(&bar.v_full[stage], v_par, abort_flag, a.status, limit) ||
+            !wait_bar(&bar.p_lo[w], par, abort_flag, a.status, limit))
+          break;
+      }
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          mma_ts(t_o, t_p + k * 8, vd + k * (16 * 128 / 16), kIdescPV, (o_i >= 2 || k) ? 1u : 0u);
+      }
+      __syncwarp();
+      if (!wait_bar(&bar.p_hi[w], par, abort_flag, a.status, limit)) break;
+      tc_fence_after();
+      const bool last_v = !o_wide || (o_i & 1);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = kTile / 32; k < kTile / 16; ++k)
+          mma_ts(t_o, t_p + k * 8, vd + k * (16 * 128 / 16), kIdescPV, 1u);
+        if (last_v) mma_commit(&bar.v_empty[stage]);
+        if (o_left <= 2) mma_commit(&bar.o_full[w]);
+      }
+      __syncwarp();
+      p_par ^= 1u << w;
+      o_tile += last_v;
+      ++o_i;
+      --o_left;
+      ++o_n;
     }
-    if (any) {
+    if (s_n > 0) {
       if (elect_one()) mma_commit(&bar.drain);
       __syncwarp();
       wait_drain(&bar.drain, 0, limit);
@@ -651,12 +735,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const float sl2 = a.scale * 1.4426950408889634f;
     const float lag = kLag / sl2;
     const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
-    uint32_t nseg = 0, s_use = 0, o_use = 0, vc = 0;
+    // segments, uses of s_full and o_full, V tiles and steps so far
+    uint32_t nseg = 0, s_use = 0, o_use = 0, vc = 0, step = 0;
     bool ok = true;
     while (ok) {
       const uint32_t r = nseg % kDescs;
-      ok = __all_sync(0xffffffffu, wait_bar(&bar.d_full[r], (nseg / kDescs) & 1u,
-                                                     abort_flag, a.status, limit));
+      ok = wait_bar(&bar.d_full[r], (nseg / kDescs) & 1u,
+                                                     abort_flag, a.status, limit);
       if (!ok) break;
       const Segment sg = bar.seg[r];
       __syncwarp();
@@ -668,118 +753,128 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int live_rows = min(max(sg.ntok - first_tok, 0), g.tpt) * g.G;
       const bool warp_live = quad * 32 < live_rows;
       const int lim = row < live_rows ? min(sg.kv_len, sg.lim0 + first_tok + row / g.G) : 1 << 30;
-      const int steps = sg.wide ? tiles : (tiles + 1 - w) / 2;
+      const int i0 = (step + w) & 1;  // the group's first step of the segment
+      const int steps = sg.wide ? tiles : (tiles + 1 - i0) / 2;
       float m = -INFINITY;
       uint64_t l2 = 0;
       for (int i = 0; i < steps; ++i) {
-        const int ti = sg.wide ? i : 2 * i + w;  // tile of the segment
+        const int ti = sg.wide ? i : 2 * i + i0;  // tile of the segment
         const int t = sg.t0 + ti;
-        ok = __all_sync(0xffffffffu, wait_bar(&bar.s_full[w], s_use & 1u, abort_flag,
-                                                       a.status, limit));
+        ok = wait_bar(&bar.s_full[w], s_use & 1u, abort_flag,
+                                                       a.status, limit);
         if (!ok) break;
         ++s_use;
         tc_fence_after();
-        if (warp_live) {
-          uint32_t v[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + c * 32, v[c]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_regs_fence(v[c]);
-          const int vis = lim - t * kTile;  // keys of the tile the row sees
-          if (__any_sync(0xffffffffu, vis < kTile)) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c * 32 + j >= vis) v[c][j] = 0xff800000u;  // -inf
-          }
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
-#pragma unroll
-          for (int j = 0; j < 32; j += 2)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float x = __uint_as_float(v[c][j]), y = __uint_as_float(v[c][j + 1]);
-              asm("max.f32 %0, %0, %1, %2;" : "+f"(tops[c]) : "f"(x), "f"(y));
-            }
-          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-          const bool moves = top > m + lag;
-          if (__any_sync(0xffffffffu, moves)) {
-            const float m1 = moves ? top : m;
-            // 0 where the row has seen nothing yet
-            const float f = moves ? ex2((m - m1) * sl2) : 1.0f;
-            m = m1;
-            const float2 lv = unpack_f32x2(l2);
-            l2 = pack_f32x2(lv.x * f, lv.y * f);
-            if (i > 0) {
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(to + c * 16, o);
-                tmem_ld_wait();
-                tmem_regs_fence16(o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st_32x32b_x16(to + c * 16, o);
-              }
-            }
-          }
-          const float c0 = m == -INFINITY ? kOff : kOff - m * sl2;
-          const uint64_t c0x2 = pack_f32x2(c0, c0);
-          uint64_t sums[4] = {l2, 0, 0, 0};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const uint64_t x = fma_f32x2(pack_f32x2(__uint_as_float(v[c][2 * j]),
-                                                      __uint_as_float(v[c][2 * j + 1])),
-                                           sl2x2, c0x2);
-              float2 e = unpack_f32x2(x);
-              e.x = ex2(e.x);
-              e.y = ex2(e.y);
-              sums[j & 3] = add_f32x2(sums[j & 3], pack_f32x2(e.x, e.y));
-              p[j] = pack2<DTYPE>(e.x, e.y);
-            }
-            tmem_st_32x32b_x16(ts + c * 16, p);
-          }
-          l2 = add_f32x2(add_f32x2(sums[0], sums[1]), add_f32x2(sums[2], sums[3]));
-          tmem_st_wait();
-        }
         // rows of V past the keys' end may hold anything, and 0 * NaN is not
-        // 0: they are cleared in shared memory before the product
+        // 0: they are cleared in shared memory before the product (in a wide
+        // unit by the group whose product comes first)
         const int valid = sg.kv_len - t * kTile;
-        if (valid < kTile && (!sg.wide || w == 0)) {
+        if (valid < kTile && (!sg.wide || i0 == 0)) {
           const uint32_t at = vc + ti;
-          ok = __all_sync(0xffffffffu,
-                          wait_bar(&bar.v_full[at % C::STAGES], (at / C::STAGES) & 1u,
-                                            abort_flag, a.status, limit));
+          ok = wait_bar(&bar.v_full[at % C::STAGES], (at / C::STAGES) & 1u, abort_flag, a.status,
+                        limit);
           if (!ok) break;
           if (row >= valid) {
-#pragma unroll
-            for (int d = 0; d < kBlocks; ++d) {
-              const uint32_t dst = smem_u32(smem + C::V_OFF + (at % C::STAGES) * C::TILE_BYTES +
-                                            d * C::BLK + row * 128);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) st_shared_v4(dst + q * 16, 0, 0, 0, 0);
-            }
+#pragma unroll 1
+            for (int q = 0; q < 8 * kBlocks; ++q)
+              st_shared_v4(smem_u32(smem + C::V_OFF + (at % C::STAGES) * C::TILE_BYTES +
+                                    (q >> 3) * C::BLK + row * 128 + (q & 7) * 16),
+                           0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[w]);
+        if (!warp_live) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar.p_lo[w]);
+            mbar_arrive(&bar.p_hi[w]);
+          }
+          continue;
+        }
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + c * 32, v[c]);
+        const int vis = lim - t * kTile;  // keys of the tile the row sees
+        const bool masked = __any_sync(0xffffffffu, vis < kTile);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_regs_fence(v[c]);
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c * 32 + j >= vis) v[c][j] = 0xff800000u;  // -inf
+        }
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float x = __uint_as_float(v[c][j]), y = __uint_as_float(v[c][j + 1]);
+            asm("max.f32 %0, %0, %1, %2;" : "+f"(tops[c]) : "f"(x), "f"(y));
+          }
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        const bool moves = top > m + lag;
+        if (__any_sync(0xffffffffu, moves)) {
+          const float m1 = moves ? top : m;
+          // 0 where the row has seen nothing yet
+          const float f = moves ? ex2((m - m1) * sl2) : 1.0f;
+          m = m1;
+          const float2 lv = unpack_f32x2(l2);
+          l2 = pack_f32x2(lv.x * f, lv.y * f);
+          if (i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(to + c * 16, o);
+              tmem_ld_wait();
+              tmem_regs_fence16(o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st_32x32b_x16(to + c * 16, o);
+            }
+          }
+        }
+        const float c0 = m == -INFINITY ? kOff : kOff - m * sl2;
+        const uint64_t c0x2 = pack_f32x2(c0, c0);
+        uint64_t sums[4] = {l2, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t x = fma_f32x2(
+                pack_f32x2(__uint_as_float(v[c][2 * j]), __uint_as_float(v[c][2 * j + 1])), sl2x2,
+                c0x2);
+            float2 e = unpack_f32x2(x);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sums[j & 3] = add_f32x2(sums[j & 3], pack_f32x2(e.x, e.y));
+            p[j] = pack2<DTYPE>(e.x, e.y);
+          }
+          tmem_st_32x32b_x16(ts + c * 16, p);
+          if (c == 1 || c == 3) {  // the MMA issuer starts on the first half
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c == 1 ? &bar.p_lo[w] : &bar.p_hi[w]);
+          }
+        }
+        l2 = add_f32x2(add_f32x2(sums[0], sums[1]), add_f32x2(sums[2], sums[3]));
       }
       if (!ok) break;
       vc += tiles;
+      step += tiles << sg.wide;
       const int64_t at = sg.slot + static_cast<int64_t>(w) * sg.rows + row;
       const bool mine = row < live_rows;
       if (steps == 0) {  // a single tile: the other group's
         if (mine) g.part_lse[at] = -INFINITY;
         continue;
       }
-      ok = __all_sync(0xffffffffu, wait_bar(&bar.o_full[w], o_use & 1u, abort_flag,
-                                                     a.status, limit));
+      ok = wait_bar(&bar.o_full[w], o_use & 1u, abort_flag,
+                                                     a.status, limit);
       if (!ok) break;
       ++o_use;
       tc_fence_after();
@@ -826,8 +921,7 @@ __global__ void __launch_bounds__(256) prefix_attention_join_kernel(const AttnAr
   constexpr int E = D / 32;
   const PrefixAttnArgs &a = g.a;
   const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const int64_t total = planned ? g.head->total : 0;
-  const int pieces = planned ? g.head->pieces : 1;
+  const int64_t piece = planned ? *g.piece : 1;
   // the token's sequence: how many end at or before it
   int b = t;
   if (a.q_offsets) {
@@ -843,7 +937,7 @@ __global__ void __launch_bounds__(256) prefix_attention_join_kernel(const AttnAr
   }
   int tiles = 0, place = 0, unit = 0;
   int64_t cum = 0;
-  if (b < a.B && total > 0) {
+  if (b < a.B && planned) {
     const SeqMeta m = g.meta[b];
     const int q0 = a.q_offsets ? a.q_offsets[b] : b;
     place = t - q0;
@@ -861,10 +955,11 @@ __global__ void __launch_bounds__(256) prefix_attention_join_kernel(const AttnAr
       const int block = t / g.p_tok, in = t - block * g.p_tok;
       const int64_t u = static_cast<int64_t>(kvh) * g.p_blocks + block;
       const int64_t start = u * g.p_cost;
-      const int c0 = piece_of(total, pieces, start);
-      const int c1 = piece_of(total, pieces,
-                              start + static_cast<int64_t>(g.p_tiles - 1) *
-                                          (g.p_wide ? kWideCost : kNarrowCost));
+      const int c0 = static_cast<int>(quotient(start, piece));
+      const int c1 = static_cast<int>(
+          quotient(start + static_cast<int64_t>(g.p_tiles - 1) *
+                               (g.p_wide ? kWideCost : kNarrowCost),
+                   piece));
       first[0] = (u + c0) * 2 * g.p_rows + (g.p_wide ? in / g.tpt * g.p_rows : 0) +
                  in % g.tpt * g.G + hg;
       n[0] = g.p_wide ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
@@ -876,8 +971,9 @@ __global__ void __launch_bounds__(256) prefix_attention_join_kernel(const AttnAr
       const int j = block * a.hkv + kvh;
       const int64_t start =
           g.p_total + cum + j * (static_cast<int64_t>(tiles) * w + kUnitCost);
-      const int c0 = piece_of(total, pieces, start);
-      const int c1 = piece_of(total, pieces, start + static_cast<int64_t>(tiles - 1) * w);
+      const int c0 = static_cast<int>(quotient(start, piece));
+      const int c1 =
+          static_cast<int>(quotient(start + static_cast<int64_t>(tiles - 1) * w, piece));
       first[1] = g.s_slot0 + (static_cast<int64_t>(unit + j) + c0) * 2 * g.s_rows +
                  (g.s_wide ? in / g.tpt * g.s_rows : 0) + in % g.tpt * g.G + hg;
       n[1] = g.s_wide ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
@@ -1018,7 +1114,7 @@ cudaError_t run(const PrefixAttnArgs &a, cudaStream_t s) {
   g.a = a;
   if (!g.a.wait_limit_ns) g.a.wait_limit_ns = kDefaultWaitLimitNs;
   const Scratch sc = plan(g, a.T, a.B, a.max_q, a.hq, a.hkv, D, a.prefix_len);
-  g.head = reinterpret_cast<PlanHeader *>(a.scratch + sc.head);
+  g.piece = reinterpret_cast<int64_t *>(a.scratch + sc.head);
   g.meta = reinterpret_cast<SeqMeta *>(a.scratch + sc.meta);
   g.part_lse = reinterpret_cast<float *>(a.scratch + sc.lse);
   g.part_o = reinterpret_cast<float *>(a.scratch + sc.o);
