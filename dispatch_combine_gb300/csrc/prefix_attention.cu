@@ -28,6 +28,7 @@
 // of one group run while the other group takes exponentials), with few the
 // cache's bytes.
 #include <algorithm>
+#include <cstddef>
 #include <mutex>
 
 #include "elem.cuh"
@@ -220,16 +221,31 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// whether the phase with this parity is complete, without waiting
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+// a condition whose code belongs out of the straight line (the loops below
+// pass through the instruction cache once per tile)
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, false); }
+
+// Barriers are addressed by their 32-bit shared-memory address.  A test of a
+// complete phase takes about 45 cycles, a try_wait about 125, so waits here
+// poll with tests.
+__device__ __forceinline__ uint32_t bar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
-  return ok != 0;
+  return ok;
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bar_commit(uint32_t bar) {  // when the MMAs so far are complete
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
 }
 // The bounded wait, out of line: its code is long, and it reads the global
 // timer, which takes about a microsecond.
@@ -237,14 +253,22 @@ __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile 
                                        uint32_t *status, uint64_t limit_ns) {
   return mbar_wait_bounded(bar, parity, abort, status, limit_ns);
 }
+// What a wait needs when it becomes long.
+struct WaitCtx {
+  uint32_t base;  // shared address of the barriers
+  uint64_t *bars;
+  volatile int *abort;
+  uint32_t *status;
+  uint64_t limit_ns;
+};
 // Whole warp: true for all lanes when the phase completed, false for all when
 // some lane gave up.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                         uint32_t *status, uint64_t limit_ns) {
+__device__ __forceinline__ bool wait_bar(const WaitCtx &c, uint32_t bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < 256; ++i)
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, wait_long(bar, parity, abort, status, limit_ns));
+  for (int i = 0; i < 2048; ++i)
+    if (__all_sync(0xffffffffu, bar_test(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_long(c.bars + (bar - c.base) / 8, parity, c.abort, c.status,
+                                           c.limit_ns));
 }
 // Time-bounded wait that ignores the abort flag (to drain after an abort).
 __device__ __noinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
@@ -269,7 +293,7 @@ struct Bars {
   uint64_t p_lo[2], p_hi[2];  // its probabilities are: keys 0-63, 64-127
   uint64_t o_full[2];  // its segment's accumulator is complete
   uint64_t d_full[kDescs], d_empty[kDescs];
-  uint64_t drain;
+  uint64_t drain[1];
   Segment seg[kDescs];
   int64_t start_cum;
   int start_seq, start_unit;
@@ -298,6 +322,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const PrefixAttnArgs &a = g.a;
   const uint64_t limit = a.wait_limit_ns;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bars = smem_u32(&bar);
+#define BAR(field, i) (bars + static_cast<uint32_t>(offsetof(B, field)) + 8u * (i))
+  const WaitCtx wc = {bars, reinterpret_cast<uint64_t *>(&bar), abort_flag, a.status, limit};
 
   // ---- where this CTA's piece of the line lies (every CTA by itself) ----
   const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
@@ -348,7 +375,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&bar.d_full[i], 1);
       mbar_init(&bar.d_empty[i], 9);
     }
-    mbar_init(&bar.drain, 1);
+    mbar_init(&bar.drain[0], 1);
     fence_mbar_init();
   }
   // offsets that are no partition of the tokens: the own rows are left out
@@ -498,18 +525,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       // publish the segment, then fetch its queries and tiles
       const uint32_t r = nseg % kDescs;
-      ok = wait_bar(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status, limit);
+      ok = wait_bar(wc, BAR(d_empty, r), ((nseg / kDescs) & 1u) ^ 1u);
       if (!ok) break;
       const int h0 = wide ? 0 : nseg & 1;  // a narrow unit's rows alternate between the buffers
       if (lane == 0) {
         bar.seg[r] = Segment{t0, t1, kv_len, wide, ntok, lim0, own ? g.s_rows : g.p_rows, slot};
-        mbar_arrive(&bar.d_full[r]);
+        bar_arrive(BAR(d_full, r));
       }
       ++nseg;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h < h0 || h > h0 + wide) continue;
-        ok = wait_bar(&bar.q_empty[h], (q_use[h] & 1u) ^ 1u, abort_flag, a.status, limit);
+        ok = wait_bar(wc, BAR(q_empty, h), (q_use[h] & 1u) ^ 1u);
         if (!ok) break;
         ++q_use[h];
         if (lane == 0) {
@@ -548,8 +575,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           uint64_t *full = which ? &bar.v_full[stage] : &bar.k_full[stage];
-          ok = wait_bar(which ? &bar.v_empty[stage] : &bar.k_empty[stage], par, abort_flag,
-                        a.status, limit);
+          ok = wait_bar(wc, which ? BAR(v_empty, stage) : BAR(k_empty, stage), par);
           if (!ok) break;
           ++issued[which];
           if (lane == 0) mbar_arrive_expect_tx(full, bytes);
@@ -568,10 +594,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (ok) {  // the end
       const uint32_t r = nseg % kDescs;
-      ok = wait_bar(&bar.d_empty[r], ((nseg / kDescs) & 1u) ^ 1u, abort_flag, a.status, limit);
+      ok = wait_bar(wc, BAR(d_empty, r), ((nseg / kDescs) & 1u) ^ 1u);
       if (ok && lane == 0) {
         bar.seg[r] = Segment{0, 0, 0, 0, 0, 0, 0, 0};
-        mbar_arrive(&bar.d_full[r]);
+        bar_arrive(BAR(d_full, r));
       }
     }
     __syncwarp();
@@ -615,11 +641,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (s_n < o_n + 2 && !end) {
         const bool alone = s_n == o_n;
         bool have = s_left > 0;
-        if (!have) {
+        if (rare(!have)) {
           const uint32_t r = s_seg % kDescs, par = (s_seg / kDescs) & 1u;
-          have = all(mbar_test(&bar.d_full[r], par));
-          if (!have && alone) {
-            have = wait_bar(&bar.d_full[r], par, abort_flag, a.status, limit);
+          have = all(bar_test(BAR(d_full, r), par));
+          if (rare(!have && alone)) {
+            have = wait_bar(wc, BAR(d_full, r), par);
             if (!have) break;
           }
           if (have) {
@@ -636,12 +662,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int w = s_n & 1, h = s_wide ? w : (s_seg - 1) & 1;
           const bool first_q = s_i <= s_wide;
           const uint32_t stage = s_tile % C::STAGES, k_par = (s_tile / C::STAGES) & 1u;
-          bool there = all(mbar_test(&bar.k_full[stage], k_par) &&
-                           (!first_q || mbar_test(&bar.q_full[h], (q_par >> h) & 1u)));
-          if (!there && alone) {
-            there = wait_bar(&bar.k_full[stage], k_par, abort_flag, a.status, limit) &&
+          bool there = all(bar_test(BAR(k_full, stage), k_par) &
+                           bar_test(BAR(q_full, h), first_q ? (q_par >> h) & 1u : ~(q_par >> h) & 1u));
+          if (rare(!there && alone)) {
+            there = wait_bar(wc, BAR(k_full, stage), k_par) &&
                     (!first_q ||
-                     wait_bar(&bar.q_full[h], (q_par >> h) & 1u, abort_flag, a.status, limit));
+                     wait_bar(wc, BAR(q_full, h), (q_par >> h) & 1u));
             if (!there) break;
           }
           if (there) {
@@ -655,9 +681,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const uint32_t at = (k / 4) * (C::BLK / 16) + 2 * (k & 3);
                 mma_bf16_ss(tmem_base + w * 128, qd + at, kd + at, kIdescQK, k ? 1u : 0u);
               }
-              mma_commit(&bar.s_full[w]);
-              if (last_k) mma_commit(&bar.k_empty[stage]);
-              if (s_left <= 1 + s_wide) mma_commit(&bar.q_empty[h]);
+              bar_commit(BAR(s_full, w));
+              if (last_k) bar_commit(BAR(k_empty, stage));
+              if (s_left <= 1 + s_wide) bar_commit(BAR(q_empty, h));
             }
             __syncwarp();
             if (first_q) q_par ^= 1u << h;
@@ -669,14 +695,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       }
-      if (s_n == o_n) break;  // the end
+      if (rare(s_n == o_n)) break;  // the end
       // ---- the next product; its first half of keys may be ready early
-      if (o_left == 0) {  // its segment was opened by the scores
+      if (rare(o_left == 0)) {  // its segment was opened by the scores
         const uint32_t r = o_seg % kDescs;
         const int tiles = __reduce_max_sync(0xffffffffu, bar.seg[r].t1 - bar.seg[r].t0);
         o_wide = __reduce_max_sync(0xffffffffu, bar.seg[r].wide);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.d_empty[r]);
+        if (lane == 0) bar_arrive(BAR(d_empty, r));
         o_left = tiles << o_wide;
         o_i = 0;
         ++o_seg;
@@ -686,9 +712,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint32_t par = (p_par >> w) & 1u;
       const uint64_t vd = desc_v + stage * (C::TILE_BYTES / 16);
       const uint32_t t_p = tmem_base + w * 128, t_o = tmem_base + 256 + w * 128;
-      if (!all(mbar_test(&bar.v_full[stage], v_par) && mbar_test(&bar.p_lo[w], par))) {
-        if (!wait_bar(&bar.v_full[stage], v_par, abort_flag, a.status, limit) ||
-            !wait_bar(&bar.p_lo[w], par, abort_flag, a.status, limit))
+      if (rare(!all(bar_test(BAR(v_full, stage), v_par) & bar_test(BAR(p_lo, w), par)))) {
+        if (!wait_bar(wc, BAR(v_full, stage), v_par) ||
+            !wait_bar(wc, BAR(p_lo, w), par))
           break;
       }
       tc_fence_after();
@@ -698,15 +724,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           mma_ts(t_o, t_p + k * 8, vd + k * (16 * 128 / 16), kIdescPV, (o_i >= 2 || k) ? 1u : 0u);
       }
       __syncwarp();
-      if (!wait_bar(&bar.p_hi[w], par, abort_flag, a.status, limit)) break;
+      if (!wait_bar(wc, BAR(p_hi, w), par)) break;
       tc_fence_after();
       const bool last_v = !o_wide || (o_i & 1);
       if (elect_one()) {
 #pragma unroll
         for (int k = kTile / 32; k < kTile / 16; ++k)
           mma_ts(t_o, t_p + k * 8, vd + k * (16 * 128 / 16), kIdescPV, 1u);
-        if (last_v) mma_commit(&bar.v_empty[stage]);
-        if (o_left <= 2) mma_commit(&bar.o_full[w]);
+        if (last_v) bar_commit(BAR(v_empty, stage));
+        if (o_left <= 2) bar_commit(BAR(o_full, w));
       }
       __syncwarp();
       p_par ^= 1u << w;
@@ -716,9 +742,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       ++o_n;
     }
     if (s_n > 0) {
-      if (elect_one()) mma_commit(&bar.drain);
+      if (elect_one()) bar_commit(BAR(drain, 0));
       __syncwarp();
-      wait_drain(&bar.drain, 0, limit);
+      wait_drain(&bar.drain[0], 0, limit);
     }
   } else {
     // ---------------- softmax: group w = warps 4w .. 4w+3, a row per thread ----------------
@@ -740,12 +766,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     while (ok) {
       const uint32_t r = nseg % kDescs;
-      ok = wait_bar(&bar.d_full[r], (nseg / kDescs) & 1u,
-                                                     abort_flag, a.status, limit);
+      ok = wait_bar(wc, BAR(d_full, r), (nseg / kDescs) & 1u);
       if (!ok) break;
       const Segment sg = bar.seg[r];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.d_empty[r]);
+      if (lane == 0) bar_arrive(BAR(d_empty, r));
       ++nseg;
       const int tiles = sg.t1 - sg.t0;
       if (tiles == 0) break;
@@ -760,8 +785,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int i = 0; i < steps; ++i) {
         const int ti = sg.wide ? i : 2 * i + i0;  // tile of the segment
         const int t = sg.t0 + ti;
-        ok = wait_bar(&bar.s_full[w], s_use & 1u, abort_flag,
-                                                       a.status, limit);
+        ok = wait_bar(wc, BAR(s_full, w), s_use & 1u);
         if (!ok) break;
         ++s_use;
         tc_fence_after();
@@ -769,10 +793,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // 0: they are cleared in shared memory before the product (in a wide
         // unit by the group whose product comes first)
         const int valid = sg.kv_len - t * kTile;
-        if (valid < kTile && (!sg.wide || i0 == 0)) {
+        if (rare(valid < kTile && (!sg.wide || i0 == 0))) {
           const uint32_t at = vc + ti;
-          ok = wait_bar(&bar.v_full[at % C::STAGES], (at / C::STAGES) & 1u, abort_flag, a.status,
-                        limit);
+          ok = wait_bar(wc, BAR(v_full, at % C::STAGES), (at / C::STAGES) & 1u);
           if (!ok) break;
           if (row >= valid) {
 #pragma unroll 1
@@ -783,12 +806,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        if (!warp_live) {
+        if (rare(!warp_live)) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bar.p_lo[w]);
-            mbar_arrive(&bar.p_hi[w]);
+            bar_arrive(BAR(p_lo, w));
+            bar_arrive(BAR(p_hi, w));
           }
           continue;
         }
@@ -800,7 +823,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_regs_fence(v[c]);
-        if (masked) {
+        if (rare(masked)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -817,7 +840,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         const bool moves = top > m + lag;
-        if (__any_sync(0xffffffffu, moves)) {
+        if (rare(__any_sync(0xffffffffu, moves))) {
           const float m1 = moves ? top : m;
           // 0 where the row has seen nothing yet
           const float f = moves ? ex2((m - m1) * sl2) : 1.0f;
@@ -859,7 +882,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(c == 1 ? &bar.p_lo[w] : &bar.p_hi[w]);
+            if (lane == 0) bar_arrive(c == 1 ? BAR(p_lo, w) : BAR(p_hi, w));
           }
         }
         l2 = add_f32x2(add_f32x2(sums[0], sums[1]), add_f32x2(sums[2], sums[3]));
@@ -873,8 +896,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (mine) g.part_lse[at] = -INFINITY;
         continue;
       }
-      ok = wait_bar(&bar.o_full[w], o_use & 1u, abort_flag,
-                                                     a.status, limit);
+      ok = wait_bar(wc, BAR(o_full, w), o_use & 1u);
       if (!ok) break;
       ++o_use;
       tc_fence_after();
@@ -909,6 +931,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem_base, 512);
+#undef BAR
 }
 
 // ---------------------------------------------------------------------------
