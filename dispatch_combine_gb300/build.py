@@ -23,7 +23,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["router.cu", "route_screen.cu", "dispatch.cu", "combine.cu", "gemm.cu", "api.cu", "noalloc.cu",
-           "quant.cu", "eplb.cpp", "norm.cu", "kv_append.cu", "prefix_attention.cu", "api_block.cu"]
+           "quant.cu", "eplb.cpp", "norm.cu", "kv_append.cu", "prefix_attention.cu",
+           "prefix_attention_rows.cu", "prefix_attention_tiles.cu", "api_block.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,311 @@
+// attention.cuh -- what the kernels of the shared-prefix attention have in
+// common: the plan of the work, and the walk over it.
+//
+// Work is cut into units: a block of tokens x a key head x the rows those
+// tokens see in one place (the shared prefix, or their sequence's own rows),
+// each a run of steps along the keys.  The units of one kind stand in a line,
+// weighted by their time, and the line is cut into pieces of one length, one
+// per worker, so the load is even whatever the lengths, which only the device
+// knows.  A unit's stretch on a worker is a segment and leaves one partial
+// result (o normalised, and its log-sum-exp); a last kernel joins them.
+// A segment's slot among the partial results is its unit's number + its
+// worker's, which grows along the line, so `units + workers` slots are enough.
+#pragma once
+
+#include "elem.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+// What the joining kernel needs of a sequence.
+struct SeqMeta {
+  int64_t cum;    // where its units start in the line
+  int32_t unit;   // number of its first unit
+  int32_t steps;  // per unit
+};
+
+// How the own rows of the sequences are cut (by either kernel).
+struct OwnPlan {
+  int tok;         // tokens of a unit
+  int step_keys;   // keys of a step
+  int step_cost, unit_cost;
+  int rows;        // rows of a slot (or of its half)
+  int64_t slot0;   // first row of its slots
+};
+
+struct AttnArgs {
+  PrefixAttnArgs a;
+  int G;  // query heads per key head
+  // rows kernel: units of up to 16 * r_mt rows, a step is a slice of 16 keys
+  int r_on, r_mt, r_tok, r_rows;
+  int r_prefix, r_blocks, r_slices;  // the prefix's units are its: token blocks, slices
+  int64_t r_pcost, r_ptotal;         // of a prefix unit, of all
+  // tiles kernel: units of up to 128 (narrow) or 256 (wide) rows, a step is a
+  // tile of 128 keys
+  int t_on, tpt;                     // tokens per 128 rows
+  int p_on, p_wide, p_tok, p_blocks, p_tiles, p_rows, p_box;
+  int p_gang, p_groups, p_gangs;     // CTAs of a gang, token blocks / gang, gangs
+  int64_t p_piece;                   // tiles of a gang's piece
+  int own_on, s_wide, s_box;
+  OwnPlan own;
+  int own_rows_kernel;               // the own rows are the rows kernel's
+  int64_t *pieces;                   // device: piece lengths (rows kernel; tiles kernel: gang CTAs, others)
+  SeqMeta *meta;
+  float *part_o, *part_lse;
+};
+
+struct Seq {
+  int q0, nq, len, steps, units;
+  int64_t cost;  // of all its units
+};
+
+// Sequence b with every value clamped into the buffers.
+__device__ __forceinline__ Seq read_seq(const AttnArgs &g, int b, bool *bad_off, bool *bad) {
+  const PrefixAttnArgs &a = g.a;
+  Seq s = {0, 0, 0, 0, 0, 0};
+  if (b >= a.B) return s;
+  s.q0 = b;
+  s.nq = 1;
+  if (a.q_offsets) {
+    const int q0 = a.q_offsets[b], q1 = a.q_offsets[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > a.T) *bad_off = true;
+    s.q0 = min(max(q0, 0), a.T);
+    s.nq = max(min(q1, a.T), s.q0) - s.q0;
+    if (s.nq > a.max_q) *bad = true;
+    s.nq = min(s.nq, a.max_q);
+  }
+  const int cap = a.max_pages << a.page_shift;
+  const int len = a.kv_lens[b];
+  if (len < 0 || len > cap) *bad = true;
+  s.len = min(max(len, 0), cap);
+  s.steps = (s.len + g.own.step_keys - 1) / g.own.step_keys;
+  s.units = (s.nq + g.own.tok - 1) / g.own.tok * a.hkv;
+  s.cost = s.steps > 0
+               ? s.units * (static_cast<int64_t>(s.steps) * g.own.step_cost + g.own.unit_cost)
+               : 0;
+  return s;
+}
+
+// 64-bit divisions are kept out of line: they are long code.
+__device__ __noinline__ inline int64_t div64(int64_t n, int64_t d) { return n / d; }
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if (n < (int64_t{1} << 31) && d < (int64_t{1} << 31))
+    return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+  return div64(n, d);
+}
+
+// Costs and unit counts of all sequences, scanned by the whole CTA (THREADS
+// threads, any number of sequences).  `before` of a thread's first sequence.
+struct OwnScan {
+  int b_lo, b_hi;
+  int64_t before, total;
+  int units_before;
+  bool drop, bad;  // offsets that are no partition of the tokens: nothing is attended
+};
+template <int THREADS>
+struct ScanShared {
+  int64_t warp_cost[THREADS / 32], before[THREADS];
+  int warp_units[THREADS / 32], units[THREADS];
+};
+template <int THREADS>
+__device__ __forceinline__ OwnScan scan_own(const AttnArgs &g, ScanShared<THREADS> &sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (g.a.B + THREADS - 1) / THREADS;
+  OwnScan r;
+  r.b_lo = threadIdx.x * per;
+  r.b_hi = min(r.b_lo + per, g.a.B);
+  int64_t my_cost = 0;
+  int my_units = 0;
+  bool bad_off = false, bad = false;
+#pragma unroll 1
+  for (int b = r.b_lo; b < r.b_hi; ++b) {
+    const Seq s = read_seq(g, b, &bad_off, &bad);
+    my_cost += s.cost;
+    my_units += s.units;
+  }
+  int64_t cost = my_cost;
+  int units = my_units;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t c = __shfl_up_sync(0xffffffffu, cost, off);
+    const int u = __shfl_up_sync(0xffffffffu, units, off);
+    if (lane >= off) {
+      cost += c;
+      units += u;
+    }
+  }
+  if (lane == 31) {
+    sh.warp_cost[warp] = cost;
+    sh.warp_units[warp] = units;
+  }
+  r.drop = __syncthreads_or(bad_off);
+  r.bad = bad || bad_off;
+  r.before = cost - my_cost;
+  r.units_before = units - my_units;
+  r.total = 0;
+#pragma unroll 1
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) {
+      r.before += sh.warp_cost[w];
+      r.units_before += sh.warp_units[w];
+    }
+    r.total += sh.warp_cost[w];
+  }
+  if (r.drop) r.total = 0;
+  sh.before[threadIdx.x] = r.before;
+  sh.units[threadIdx.x] = r.units_before;
+  __syncthreads();
+  return r;
+}
+// The scan's values of each sequence for the joining kernel (one CTA).
+__device__ __forceinline__ void write_meta(const AttnArgs &g, const OwnScan &r) {
+  bool x = false, y = false;
+  int64_t cum = r.before;
+  int unit = r.units_before;
+#pragma unroll 1
+  for (int b = r.b_lo; b < r.b_hi; ++b) {
+    const Seq s = read_seq(g, b, &x, &y);
+    g.meta[b] = SeqMeta{cum, unit, r.drop ? 0 : s.steps};
+    cum += s.cost;
+    unit += s.units;
+  }
+  if (r.bad) set_status(g.a.status, kStatusBadId);
+}
+
+// A unit's stretch on one worker.
+struct Stretch {
+  int head, tok0, ntok;  // key head, first token, tokens
+  int lim0, kv_len;      // token i sees keys below min(kv_len, lim0 + i)
+  int s0, s1;            // steps
+  int64_t unit;          // its number among the units of its kind
+  const int32_t *pages;
+};
+
+// steps [s0, s1) of a unit that starts at `start`, with n steps, in [lo, hi)
+__device__ __forceinline__ int step_at(int64_t ahead, int n, int cost) {
+  if (ahead <= 0) return 0;
+  if (ahead >= static_cast<int64_t>(n) * cost) return n;
+  return (static_cast<int>(ahead) + cost - 1) / cost;
+}
+
+// Walks the own units in [lo, hi) of their line; a whole warp.  next() gives
+// one stretch at a time.
+struct OwnWalk {
+  int64_t lo, hi, cum0, batch, cum, start, unit_cost;
+  int unit0, batch_units, base, un;
+  unsigned todo;
+  Seq s;
+  int seq, j, n_units, q0, nq, len, steps, unit;
+
+  template <int THREADS>
+  __device__ __forceinline__ void begin(const AttnArgs &g, const ScanShared<THREADS> &sh,
+                                        int64_t lo_, int64_t hi_) {
+    lo = lo_;
+    hi = hi_;
+    // the last thread of the scan whose sequences start at or before lo
+    int i = 0;
+    for (int k = threadIdx.x & 31; k < THREADS; k += 32)
+      if (sh.before[k] <= lo) i = k;
+    i = __reduce_max_sync(0xffffffffu, i);
+    base = i * ((g.a.B + THREADS - 1) / THREADS) - 32;
+    cum0 = sh.before[i];
+    unit0 = sh.units[i];
+    batch = 0;
+    batch_units = 0;
+    todo = 0;
+    j = n_units = 0;
+    start = 0;
+    unit_cost = 1;
+  }
+  __device__ __forceinline__ bool next(const AttnArgs &g, Stretch *out) {
+    const int lane = threadIdx.x & 31;
+    while (true) {
+      if (j < n_units && start + j * unit_cost < hi) {
+        const int at = j++;
+        const int64_t from = start + at * unit_cost;
+        out->s0 = step_at(lo - from, steps, g.own.step_cost);
+        out->s1 = step_at(hi - from, steps, g.own.step_cost);
+        if (out->s0 >= out->s1) continue;
+        const int block = at / g.a.hkv;
+        out->head = at - block * g.a.hkv;
+        const int i0 = block * g.own.tok;
+        out->tok0 = q0 + i0;
+        out->ntok = min(g.own.tok, nq - i0);
+        out->lim0 = len - nq + i0 + 1;
+        out->kv_len = len;
+        out->unit = unit + at;
+        out->pages = g.a.page_table + static_cast<int64_t>(seq) * g.a.max_pages;
+        return true;
+      }
+      if (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        seq = base + src;
+        q0 = __shfl_sync(0xffffffffu, s.q0, src);
+        nq = __shfl_sync(0xffffffffu, s.nq, src);
+        len = __shfl_sync(0xffffffffu, s.len, src);
+        steps = __shfl_sync(0xffffffffu, s.steps, src);
+        n_units = __shfl_sync(0xffffffffu, s.units, src);
+        start = __shfl_sync(0xffffffffu, cum, src);
+        unit = __shfl_sync(0xffffffffu, un, src);
+        unit_cost = static_cast<int64_t>(steps) * g.own.step_cost + g.own.unit_cost;
+        j = lo <= start ? 0 : static_cast<int>(quotient(lo - start, unit_cost));
+        continue;
+      }
+      base += 32;
+      cum0 += batch;
+      unit0 += batch_units;
+      if (base >= g.a.B || cum0 >= hi) return false;
+      bool x = false, y = false;
+      s = read_seq(g, base + lane, &x, &y);
+      cum = s.cost;
+      un = s.units;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t c = __shfl_up_sync(0xffffffffu, cum, off);
+        const int v = __shfl_up_sync(0xffffffffu, un, off);
+        if (lane >= off) {
+          cum += c;
+          un += v;
+        }
+      }
+      batch = __shfl_sync(0xffffffffu, cum, 31);
+      batch_units = __shfl_sync(0xffffffffu, un, 31);
+      cum += cum0 - s.cost;
+      un += unit0 - s.units;
+      todo = __ballot_sync(0xffffffffu, s.cost > 0 && cum < hi && cum + s.cost > lo);
+    }
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The probabilities of both kernels are 2^(s * sl2 - m * sl2 + off): fp16 ones
+// are kept 2^10 up, away from its subnormals; the running maximum m may lag
+// by `lag` powers of two behind the true one before sums and accumulators are
+// rescaled, so they stay below 2^15 (fp16 holds 65504) or 2^8 (bf16).
+template <int DTYPE>
+struct Prob {
+  static constexpr float kOff = DTYPE == MOE_DTYPE_FP16 ? 10.0f : 0.0f;
+  static constexpr float kLag = DTYPE == MOE_DTYPE_FP16 ? 5.0f : 8.0f;
+};
+constexpr float kLog2e = 1.4426950408889634f;
+
+constexpr int kTile = 128;      // keys per tile of the tiles kernel
+constexpr int kSlice = 16;      // keys per slice of the rows kernel
+constexpr int kMaxCtas = 160;   // grid limit of both (slots of partial results)
+constexpr int kRowWarps = 8;    // warps per CTA of the rows kernel
+constexpr int kMinSlices = 4;   // shortest piece of the rows kernel's line
+constexpr int kSliceUnit = 2;   // cost of starting a unit there, in slices
+constexpr int kWideCost = 3, kNarrowCost = 2, kTileUnit = 1;  // tiles kernel
+
+// prefix_attention_rows.cu, prefix_attention_tiles.cu
+cudaError_t launch_attention_rows(const AttnArgs &g, int dtype, int ctas, cudaStream_t s);
+cudaError_t launch_attention_tiles(const AttnArgs &g, int dtype, int ctas, bool after_rows,
+                                   cudaStream_t s);
+
+}  // namespace moe
