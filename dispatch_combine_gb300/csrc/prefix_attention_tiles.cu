@@ -27,7 +27,7 @@
 namespace moe {
 namespace {
 
-constexpr int kAttnThreads = 320;  // 8 softmax warps, the loader, the MMA issuer
+constexpr int kAttnThreads = 352;  // 8 softmax warps, the loader, two MMA issuers
 constexpr int kDescs = 4;          // segments the loader may be ahead
 
 template <int D>
@@ -207,7 +207,7 @@ struct Bars {
   uint64_t p_lo[2], p_hi[2];  // its probabilities are: keys 0-63, 64-127
   uint64_t o_full[2];  // its segment's accumulator is complete
   uint64_t d_full[kDescs], d_empty[kDescs];
-  uint64_t drain[1];
+  uint64_t drain[2];
   Segment seg[kDescs];
   uint32_t tmem;
   int abort;
@@ -248,13 +248,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bar.abort = 0;
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&bar.k_full[s], 1);
-      mbar_init(&bar.k_empty[s], 1);
+      mbar_init(&bar.k_empty[s], 2);
       mbar_init(&bar.v_full[s], 1);
-      mbar_init(&bar.v_empty[s], 1);
+      mbar_init(&bar.v_empty[s], 2);
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bar.q_full[h], 1);
-      mbar_init(&bar.q_empty[h], 1);
+      mbar_init(&bar.q_empty[h], 2);
       mbar_init(&bar.s_full[h], 1);
       mbar_init(&bar.p_lo[h], 4);
       mbar_init(&bar.p_hi[h], 4);
@@ -262,9 +262,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(&bar.d_full[i], 1);
-      mbar_init(&bar.d_empty[i], 9);
+      mbar_init(&bar.d_empty[i], 10);
     }
     mbar_init(&bar.drain[0], 1);
+    mbar_init(&bar.drain[1], 1);
     fence_mbar_init();
   }
   // ---- what this CTA does: gang member `member` of gang `gang` (in the
@@ -442,137 +443,134 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       if (q_use[h]) wait_drain(&bar.q_full[h], (q_use[h] - 1) & 1u, limit);
-  } else if (warp == 9) {
-    // ---------------- MMA issuer ----------------
-    // Steps are numbered through all segments; step n belongs to group n & 1.
-    // Scores run up to two steps ahead of products with V: scores(n + 2)
-    // overwrite the probabilities of step n, so they follow product(n) (MMAs
-    // complete in issue order).  Issuing takes as long as computing (64 cycles
-    // for 128 x 128 x 16) except for the last four, the depth of the queue in
-    // front of the tensor cores, so what lies between two batches must stay
-    // below 256 cycles.  The whole warp walks the steps, so that operands stay
-    // warp-uniform, and one elected lane issues.
+  } else if (warp >= 9) {
+    // ---------------- MMA issuers: warp 9 + w for group w ----------------
+    // A product of 128 x 128 x 16 takes 64 cycles and the queue in front of
+    // the tensor cores holds four, so what an issuer does between its batches
+    // (barrier tests of 50 cycles, forming operands) would show; with a warp
+    // per group it is hidden behind the other group's products.  The whole
+    // warp walks the steps, so that operands stay warp-uniform, and one elected
+    // lane issues.  A group's scores for its next step overwrite the
+    // probabilities of this one, and follow its product with V in issue order.
     constexpr uint32_t kIdescQK = attn_idesc<DTYPE>(128, kTile, false);
     constexpr uint32_t kIdescPV = attn_idesc<DTYPE>(128, D, true);
     const uint64_t desc_q = sw128_kmajor_desc(smem_u32(smem));
     const uint64_t desc_k = sw128_kmajor_desc(smem_u32(smem + C::K_OFF));
     const uint64_t desc_v = sw128_nmajor_desc(smem_u32(smem + C::V_OFF), C::BLK);
-    // cursors of the scores and of the products: steps done, segments opened,
-    // tiles done, steps left in the segment, step in the segment, its width
-    uint32_t s_n = 0, s_seg = 0, s_tile = 0, o_n = 0, o_seg = 0, o_tile = 0;
-    int s_left = 0, s_i = 0, s_wide = 0, o_left = 0, o_i = 0, o_wide = 0;
-    uint32_t q_par = 0, p_par = 0;  // a bit per buffer / group
-    bool end = false;
+    const int w = warp - 9;
+    const uint32_t t_s = tmem_base + w * 128, t_o = tmem_base + 256 + w * 128;
+    uint32_t nseg = 0, step = 0, p_use = 0, k_tile = 0, v_tile = 0;
+    uint32_t q_par = 0;  // a bit per query buffer
+    bool ok = true, any = false;
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-    while (true) {
-      // ---- the next scores, if everything is there (or nothing else can be done)
-      if (s_n < o_n + 2 && !end) {
-        const bool alone = s_n == o_n;
-        bool have = s_left > 0;
-        if (rare(!have)) {
-          const uint32_t r = s_seg % kDescs, par = (s_seg / kDescs) & 1u;
-          have = all(bar_test(BAR(d_full, r), par));
-          if (rare(!have && alone)) {
-            have = wait_bar(wc, BAR(d_full, r), par);
-            if (!have) break;
-          }
-          if (have) {
-            const int tiles = __reduce_max_sync(0xffffffffu, bar.seg[r].t1 - bar.seg[r].t0);
-            s_wide = __reduce_max_sync(0xffffffffu, bar.seg[r].wide);
-            s_left = tiles << s_wide;
-            s_i = 0;
-            ++s_seg;
-            end = tiles == 0;
-            if (end) continue;
-          }
-        }
-        if (have) {
-          const int w = s_n & 1, h = s_wide ? w : (s_seg - 1) & 1;
-          const bool first_q = s_i <= s_wide;
-          const uint32_t stage = s_tile % C::STAGES, k_par = (s_tile / C::STAGES) & 1u;
-          bool there = all(bar_test(BAR(k_full, stage), k_par) &
-                           bar_test(BAR(q_full, h), first_q ? (q_par >> h) & 1u : ~(q_par >> h) & 1u));
-          if (rare(!there && alone)) {
-            there = wait_bar(wc, BAR(k_full, stage), k_par) &&
-                    (!first_q ||
-                     wait_bar(wc, BAR(q_full, h), (q_par >> h) & 1u));
-            if (!there) break;
-          }
-          if (there) {
-            tc_fence_after();
-            const uint64_t qd = desc_q + static_cast<uint32_t>(h * (C::TILE_BYTES / 16));
-            const uint64_t kd = desc_k + stage * (C::TILE_BYTES / 16);
-            const bool last_k = !s_wide || (s_i & 1);
-            if (elect_one()) {
+    // Both groups pass every tile and query buffer in order, and each arrives
+    // once on its release (without an MMA where it does not use it), so a
+    // buffer's phase never runs ahead of a group that has not looked at it.
+    auto skip_k = [&]() {
+      const uint32_t st = k_tile % C::STAGES;
+      ok = ok && wait_bar(wc, BAR(k_full, st), (k_tile / C::STAGES) & 1u);
+      if (ok && lane == 0) bar_arrive(BAR(k_empty, st));
+      ++k_tile;
+    };
+    auto skip_v = [&]() {
+      const uint32_t st = v_tile % C::STAGES;
+      ok = ok && wait_bar(wc, BAR(v_full, st), (v_tile / C::STAGES) & 1u);
+      if (ok && lane == 0) bar_arrive(BAR(v_empty, st));
+      ++v_tile;
+    };
+    auto skip_q = [&](int h) {
+      ok = ok && wait_bar(wc, BAR(q_full, h), (q_par >> h) & 1u);
+      if (ok && lane == 0) bar_arrive(BAR(q_empty, h));
+      q_par ^= 1u << h;
+    };
+    while (ok) {
+      const uint32_t r = nseg % kDescs;
+      ok = wait_bar(wc, BAR(d_full, r), (nseg / kDescs) & 1u);
+      if (!ok) break;
+      const int tiles = __reduce_max_sync(0xffffffffu, bar.seg[r].t1 - bar.seg[r].t0);
+      const int wide = __reduce_max_sync(0xffffffffu, bar.seg[r].wide);
+      __syncwarp();
+      if (lane == 0) bar_arrive(BAR(d_empty, r));
+      if (tiles == 0) break;
+      const int i0 = (step + w) & 1;      // the group's first step of the segment
+      const int n = wide ? tiles : (tiles + 1 - i0) / 2;
+      const int h = wide ? w : nseg & 1;  // its query buffer
+      const uint32_t k_end = k_tile + tiles, v_end = v_tile + tiles;
+      step += tiles << wide;
+      ++nseg;
+      const uint64_t qd = desc_q + static_cast<uint32_t>(h * (C::TILE_BYTES / 16));
+      auto scores = [&](bool last) {
+        const uint32_t st = k_tile % C::STAGES;
+        ok = ok && wait_bar(wc, BAR(k_full, st), (k_tile / C::STAGES) & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t kd = desc_k + st * (C::TILE_BYTES / 16);
+        if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t at = (k / 4) * (C::BLK / 16) + 2 * (k & 3);
-                mma_bf16_ss(tmem_base + w * 128, qd + at, kd + at, kIdescQK, k ? 1u : 0u);
-              }
-              bar_commit(BAR(s_full, w));
-              if (last_k) bar_commit(BAR(k_empty, stage));
-              if (s_left <= 1 + s_wide) bar_commit(BAR(q_empty, h));
-            }
-            __syncwarp();
-            if (first_q) q_par ^= 1u << h;
-            s_tile += last_k;
-            ++s_i;
-            --s_left;
-            ++s_n;
-            continue;
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = (k / 4) * (C::BLK / 16) + 2 * (k & 3);
+            mma_bf16_ss(t_s, qd + at, kd + at, kIdescQK, k ? 1u : 0u);
           }
+          bar_commit(BAR(s_full, w));
+          bar_commit(BAR(k_empty, st));
+          if (last) bar_commit(BAR(q_empty, h));
         }
-      }
-      if (rare(s_n == o_n)) break;  // the end
-      // ---- the next product; its first half of keys may be ready early
-      if (rare(o_left == 0)) {  // its segment was opened by the scores
-        const uint32_t r = o_seg % kDescs;
-        const int tiles = __reduce_max_sync(0xffffffffu, bar.seg[r].t1 - bar.seg[r].t0);
-        o_wide = __reduce_max_sync(0xffffffffu, bar.seg[r].wide);
         __syncwarp();
-        if (lane == 0) bar_arrive(BAR(d_empty, r));
-        o_left = tiles << o_wide;
-        o_i = 0;
-        ++o_seg;
+        any = true;
+        ++k_tile;
+      };
+      if (n > 0) {
+        if (!wide && i0) skip_k();
+        ok = ok && wait_bar(wc, BAR(q_full, h), (q_par >> h) & 1u);
+        q_par ^= 1u << h;
+        scores(n == 1);
+      } else {
+        skip_q(h);
       }
-      const int w = o_n & 1;
-      const uint32_t stage = o_tile % C::STAGES, v_par = (o_tile / C::STAGES) & 1u;
-      const uint32_t par = (p_par >> w) & 1u;
-      const uint64_t vd = desc_v + stage * (C::TILE_BYTES / 16);
-      const uint32_t t_p = tmem_base + w * 128, t_o = tmem_base + 256 + w * 128;
-      if (rare(!all(bar_test(BAR(v_full, stage), v_par) & bar_test(BAR(p_lo, w), par)))) {
-        if (!wait_bar(wc, BAR(v_full, stage), v_par) ||
-            !wait_bar(wc, BAR(p_lo, w), par))
-          break;
-      }
-      tc_fence_after();
-      if (elect_one()) {
+#pragma unroll 1
+      for (int i = 0; ok && i < n; ++i) {
+        if (!wide && (i || i0)) skip_v();
+        const uint32_t st = v_tile % C::STAGES, v_par = (v_tile / C::STAGES) & 1u;
+        const uint32_t p_par = p_use & 1u;
+        if (!ok) break;
+        if (!all(bar_test(BAR(v_full, st), v_par) & bar_test(BAR(p_lo, w), p_par))) {
+          ok = wait_bar(wc, BAR(v_full, st), v_par) && wait_bar(wc, BAR(p_lo, w), p_par);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint64_t vd = desc_v + st * (C::TILE_BYTES / 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTile / 32; ++k)
-          mma_ts(t_o, t_p + k * 8, vd + k * (16 * 128 / 16), kIdescPV, (o_i >= 2 || k) ? 1u : 0u);
-      }
-      __syncwarp();
-      if (!wait_bar(wc, BAR(p_hi, w), par)) break;
-      tc_fence_after();
-      const bool last_v = !o_wide || (o_i & 1);
-      if (elect_one()) {
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_ts(t_o, t_s + k * 8, vd + k * (16 * 128 / 16), kIdescPV, (i || k) ? 1u : 0u);
+        }
+        __syncwarp();
+        ok = wait_bar(wc, BAR(p_hi, w), p_par);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = kTile / 32; k < kTile / 16; ++k)
-          mma_ts(t_o, t_p + k * 8, vd + k * (16 * 128 / 16), kIdescPV, 1u);
-        if (last_v) bar_commit(BAR(v_empty, stage));
-        if (o_left <= 2) bar_commit(BAR(o_full, w));
+          for (int k = kTile / 32; k < kTile / 16; ++k)
+            mma_ts(t_o, t_s + k * 8, vd + k * (16 * 128 / 16), kIdescPV, 1u);
+          bar_commit(BAR(v_empty, st));
+          if (i == n - 1) bar_commit(BAR(o_full, w));
+        }
+        __syncwarp();
+        ++p_use;
+        ++v_tile;
+        if (i + 1 < n) {
+          if (!wide) skip_k();
+          scores(i + 2 == n);
+        }
       }
-      __syncwarp();
-      p_par ^= 1u << w;
-      o_tile += last_v;
-      ++o_i;
-      --o_left;
-      ++o_n;
+      if (wide && ok) skip_q(1 - w);
+      while (ok && k_tile != k_end) skip_k();
+      while (ok && v_tile != v_end) skip_v();
     }
-    if (s_n > 0) {
-      if (elect_one()) bar_commit(BAR(drain, 0));
+    if (any) {
+      if (elect_one()) bar_commit(BAR(drain, w));
       __syncwarp();
-      wait_drain(&bar.drain[0], 0, limit);
+      wait_drain(&bar.drain[w], 0, limit);
     }
   } else {
     // ---------------- softmax: group w = warps 4w .. 4w+3, a row per thread ----------------
@@ -613,20 +611,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ++s_use;
         tc_fence_after();
         // rows of V past the keys' end may hold anything, and 0 * NaN is not
-        // 0: they are cleared in shared memory before the product (in a wide
-        // unit by the group whose product comes first)
+        // 0: they are cleared in shared memory before the product (by both
+        // groups of a wide unit, whose products are not ordered)
         const int valid = sg.kv_len - t * kTile;
-        if (rare(valid < kTile && (!sg.wide || i0 == 0))) {
+        if (rare(valid < kTile)) {
           const uint32_t at = vc + ti;
           ok = wait_bar(wc, BAR(v_full, at % C::STAGES), (at / C::STAGES) & 1u);
           if (!ok) break;
-          if (row >= valid) {
+          const uint32_t v0 = smem_u32(smem + C::V_OFF + (at % C::STAGES) * C::TILE_BYTES);
 #pragma unroll 1
-            for (int q = 0; q < 8 * kBlocks; ++q)
-              st_shared_v4(smem_u32(smem + C::V_OFF + (at % C::STAGES) * C::TILE_BYTES +
-                                    (q >> 3) * C::BLK + row * 128 + (q & 7) * 16),
-                           0, 0, 0, 0);
-          }
+          for (int c = valid * 8 + row; c < kTile * 8; c += 128)  // 16 bytes each, consecutive
+#pragma unroll
+            for (int d = 0; d < kBlocks; ++d) st_shared_v4(v0 + d * C::BLK + c * 16, 0, 0, 0, 0);
           fence_proxy_async_smem();
         }
         if (rare(!warp_live)) {
