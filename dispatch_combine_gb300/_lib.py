@@ -10,6 +10,7 @@ PyTorch CUDA stream unless one is given.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -189,8 +190,15 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a Stream object (a few
+# microseconds less per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -685,26 +693,49 @@ def _dtype(t):
     return _DTYPES[t]
 
 
-def _rows(t, dtype, shape, name):
-    """Pointer and row stride of a tensor whose rows (its first dimension) may
-    be strided, each row dense."""
+def _refuse_rows(t, dtype, shape, name):
+    """Raises what is wrong with a row tensor (one that _rows did not take)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     _expect(t, dtype, shape, name)
     if not t.is_cuda:
         raise ValueError(f"{name}: tensor must be on a CUDA device")
-    width = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and st != width:
-            raise ValueError(f"{name}: each row must be dense")
-        width *= n
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if t.shape[0] > 1 else width)
+    raise ValueError(f"{name}: each row must be dense")
 
 
-def _vec(t, dtype, n, name):
-    if t is not None:
-        _expect(t, dtype, (n,), name)
-    return _ptr(t)
+def _rows(t, dtype, shape, name):
+    """Address and row stride of a tensor whose rows (its first dimension) may
+    be strided, each row dense."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda:
+        st = t.stride()
+        width = shape[-1]
+        if len(shape) == 3:
+            if (st[1] == width or shape[1] == 1) and (st[2] == 1 or width == 1):
+                width *= shape[1]
+                return t.data_ptr(), st[0] if shape[0] > 1 else width
+        elif st[1] == 1 or width == 1:
+            return t.data_ptr(), st[0] if shape[0] > 1 else width
+    _refuse_rows(t, dtype, shape, name)
+
+
+def _dense(t, dtype, shape, name):
+    """Address of a dense tensor; None for None."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t)
+    _expect(t, dtype, shape, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_struct(T, d, kind, dtype, eps, weight_offset):
+    return ctypes.byref(MoeNorm(T, d, kind, dtype, eps, weight_offset))
+
+
+def _fn(name):
+    return getattr(_lib if _lib is not None else lib(), name)
 
 
 def moe_norm_in(x, weight=None, bias=None, kind=MOE_NORM_RMS, eps=1e-6, weight_offset=0.0,
@@ -712,15 +743,16 @@ def moe_norm_in(x, weight=None, bias=None, kind=MOE_NORM_RMS, eps=1e-6, weight_o
     """out = N(x) * (weight + weight_offset) + bias over the rows of x [T,d]."""
     if x.dim() != 2:
         raise ValueError("x: expected [T, d]")
-    T, d = x.shape
-    n = MoeNorm(T, d, int(kind), _dtype(x.dtype), float(eps), float(weight_offset))
+    shape, dt = x.shape, x.dtype
+    n = _norm_struct(shape[0], shape[1], int(kind), _dtype(dt), float(eps), float(weight_offset))
     if out is None:
-        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
-    xp, xs = _rows(x, x.dtype, (T, d), "x")
-    op, os_ = _rows(out, x.dtype, (T, d), "out")
+        out = torch.empty(shape, dtype=dt, device=x.device)
+    xp, xs = _rows(x, dt, shape, "x")
+    op, os_ = _rows(out, dt, shape, "out")
+    vec = shape[1:]
     _check("moe_norm_in",
-           lib().moe_norm_in(ctypes.byref(n), xp, xs, _vec(weight, x.dtype, d, "weight"),
-                             _vec(bias, x.dtype, d, "bias"), op, os_, _stream(stream)))
+           _fn("moe_norm_in")(n, xp, xs, _dense(weight, dt, vec, "weight"),
+                              _dense(bias, dt, vec, "bias"), op, os_, _stream(stream)))
     return out
 
 
@@ -735,42 +767,43 @@ def moe_norm_out(f, x, post_weight=None, post_bias=None, gate=None, residual_sca
     Returns (x_out, next_out or None)."""
     if x.dim() != 2:
         raise ValueError("x: expected [T, d]")
-    T, d = x.shape
-    dt = x.dtype
-    n = MoeNorm(T, d, int(kind), _dtype(dt), float(eps), float(weight_offset))
+    shape, dt = x.shape, x.dtype
+    T, d = shape
+    n = _norm_struct(T, d, int(kind), _dtype(dt), float(eps), float(weight_offset))
     if post_norm is None:
         post_norm = post_weight is not None
     if next_norm is None:
         next_norm = next_weight is not None or next_out is not None
     gate_kind, gp, gs = MOE_GATE_NONE, None, 0
     if gate is not None:
-        if gate.dim() == 2 and tuple(gate.shape) == (T, d) and d > 1:
+        gshape = tuple(gate.shape)
+        if gshape == (T, d) and d > 1:
             gate_kind = MOE_GATE_FULL
-            gp, gs = _rows(gate, dt, (T, d), "gate")
-        elif gate.dim() == 1 and gate.shape[0] == d:
-            gate_kind, gp = MOE_GATE_CHANNEL, _vec(gate, dt, d, "gate")
+            gp, gs = _rows(gate, dt, shape, "gate")
+        elif gshape == (d,):
+            gate_kind, gp = MOE_GATE_CHANNEL, _dense(gate, dt, gshape, "gate")
+        elif gshape in ((T,), (T, 1)):
+            gate_kind, gp = MOE_GATE_TOKEN, _dense(gate.contiguous(), dt, gshape, "gate")
         else:
-            if tuple(gate.shape) not in ((T,), (T, 1)):
-                raise ValueError(f"gate: expected [{d}], [{T}], [{T}, 1] or [{T}, {d}], got "
-                                 f"{tuple(gate.shape)}")
-            gate_kind, gp = MOE_GATE_TOKEN, _vec(gate.reshape(-1), dt, T, "gate")
+            raise ValueError(f"gate: expected [{d}], [{T}], [{T}, 1] or [{T}, {d}], got {gshape}")
     if x_out is None:
-        x_out = torch.empty((T, d), dtype=dt, device=x.device)
+        x_out = torch.empty(shape, dtype=dt, device=x.device)
     np_, ns = None, 0
     if next_norm:
         if next_out is None:
-            next_out = torch.empty((T, d), dtype=dt, device=x.device)
-        np_, ns = _rows(next_out, dt, (T, d), "next_out")
-    fp, fs = _rows(f, dt, (T, d), "f")
-    xp, xs = _rows(x, dt, (T, d), "x")
-    xo, xos = _rows(x_out, dt, (T, d), "x_out")
+            next_out = torch.empty(shape, dtype=dt, device=x.device)
+        np_, ns = _rows(next_out, dt, shape, "next_out")
+    fp, fs = _rows(f, dt, shape, "f")
+    xp, xs = _rows(x, dt, shape, "x")
+    xo, xos = _rows(x_out, dt, shape, "x_out")
+    vec = shape[1:]
     _check("moe_norm_out",
-           lib().moe_norm_out(ctypes.byref(n), fp, fs, xp, xs, int(bool(post_norm)),
-                              _vec(post_weight, dt, d, "post_weight"),
-                              _vec(post_bias, dt, d, "post_bias"), gate_kind, gp, gs,
-                              float(residual_scale), _vec(next_weight, dt, d, "next_weight"),
-                              _vec(next_bias, dt, d, "next_bias"), xo, xos, np_, ns,
-                              _stream(stream)))
+           _fn("moe_norm_out")(n, fp, fs, xp, xs, 1 if post_norm else 0,
+                               _dense(post_weight, dt, vec, "post_weight"),
+                               _dense(post_bias, dt, vec, "post_bias"), gate_kind, gp, gs,
+                               residual_scale, _dense(next_weight, dt, vec, "next_weight"),
+                               _dense(next_bias, dt, vec, "next_bias"), xo, xos, np_, ns,
+                               _stream(stream)))
     return x_out, next_out if next_norm else None
 
 
@@ -784,40 +817,36 @@ def _kv_dtype(kv):
     return torch.bfloat16 if kv.dtype == MOE_DTYPE_BF16 else torch.float16
 
 
-def _caches(kv, k_cache, v_cache):
-    shape = (kv.num_pages, kv.num_kv_heads, kv.page_size, kv.head_dim)
-    _expect(k_cache, _kv_dtype(kv), shape, "k_cache")
-    _expect(v_cache, _kv_dtype(kv), shape, "v_cache")
-    return _ptr(k_cache), _ptr(v_cache)
-
-
 def moe_kv_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cache,
                   ws: Workspace = None, style=MOE_ROPE_HALF, q_out=None, stream=None):
     """Rotate q [T, Hq, D] (returned, or None when q is None) and k [T, Hkv,
     D] by their positions and append k and v to the cache at `slots`.  The
     first 2 * len(inv_freq) elements of each head turn (inv_freq None: none)."""
     dt = _kv_dtype(kv)
-    T = k.shape[0]
+    T, D, hkv = k.shape[0], kv.head_dim, kv.num_kv_heads
     qp, qs, qo, qos = None, 0, None, 0
     if q is not None:
-        qp, qs = _rows(q, dt, (T, kv.num_q_heads, kv.head_dim), "q")
+        shape = (T, kv.num_q_heads, D)
+        qp, qs = _rows(q, dt, shape, "q")
         if q_out is None:
-            q_out = torch.empty((T, kv.num_q_heads, kv.head_dim), dtype=dt, device=q.device)
-        qo, qos = _rows(q_out, dt, (T, kv.num_q_heads, kv.head_dim), "q_out")
-    kp, ks = _rows(k, dt, (T, kv.num_kv_heads, kv.head_dim), "k")
-    vp, vs = _rows(v, dt, (T, kv.num_kv_heads, kv.head_dim), "v")
-    rot = 0
+            q_out = torch.empty(shape, dtype=dt, device=q.device)
+        qo, qos = _rows(q_out, dt, shape, "q_out")
+    shape = (T, hkv, D)
+    kp, ks = _rows(k, dt, shape, "k")
+    vp, vs = _rows(v, dt, shape, "v")
+    rot, fp, pp = 0, None, None
     if inv_freq is not None:
-        _expect(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq")
-        _expect(positions, torch.int32, (T,), "positions")
         rot = 2 * inv_freq.numel()
-    _expect(slots, torch.int32, (T,), "slots")
-    kc, vc = _caches(kv, k_cache, v_cache)
+        fp = _dense(inv_freq, torch.float32, (rot // 2,), "inv_freq")
+        pp = _dense(positions, torch.int32, (T,), "positions")
+    cache = (kv.num_pages, hkv, kv.page_size, D)
     _check("moe_kv_append",
-           lib().moe_kv_append(ctypes.byref(kv), T, qp, qs, kp, ks, vp, vs, _ptr(positions),
-                               _ptr(slots), _ptr(inv_freq), rot, int(style), kc, vc, qo, qos,
-                               ws.c_ptr if ws is not None else None,
-                               ws.nbytes if ws is not None else 0, _stream(stream)))
+           _fn("moe_kv_append")(ctypes.byref(kv), T, qp, qs, kp, ks, vp, vs, pp,
+                                _dense(slots, torch.int32, (T,), "slots"), fp, rot, style,
+                                _dense(k_cache, dt, cache, "k_cache"),
+                                _dense(v_cache, dt, cache, "v_cache"), qo, qos,
+                                ws.ptr if ws is not None else None,
+                                ws.nbytes if ws is not None else 0, _stream(stream)))
     return q_out if q is not None else None
 
 
@@ -838,38 +867,37 @@ def moe_prefix_attention(kv: MoeKv, q, k_cache, v_cache, prefix_pages, prefix_le
     rows (see moe_prefix_attention in moe.h; scale defaults to D ** -0.5).
     Returns (out, lse or None)."""
     dt = _kv_dtype(kv)
-    T, B = q.shape[0], kv_lens.shape[0]
+    T, B, hq = q.shape[0], kv_lens.shape[0], kv.num_q_heads
+    shape = (T, hq, kv.head_dim)
     if out is None:
-        out = torch.empty((T, kv.num_q_heads, kv.head_dim), dtype=dt, device=q.device)
+        out = torch.empty(shape, dtype=dt, device=q.device)
     if lse is None and want_lse:
-        lse = torch.empty((T, kv.num_q_heads), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _expect(lse, torch.float32, (T, kv.num_q_heads), "lse")
-    qp, qs = _rows(q, dt, (T, kv.num_q_heads, kv.head_dim), "q")
-    op, os_ = _rows(out, dt, (T, kv.num_q_heads, kv.head_dim), "out")
-    kc, vc = _caches(kv, k_cache, v_cache)
-    _expect(kv_lens, torch.int32, (B,), "kv_lens")
-    max_pages = 0
+        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+    qp, qs = _rows(q, dt, shape, "q")
+    op, os_ = _rows(out, dt, shape, "out")
+    cache = (kv.num_pages, kv.num_kv_heads, kv.page_size, kv.head_dim)
+    max_pages, table = 0, None
     if page_table is not None:
         max_pages = page_table.shape[1]
-        _expect(page_table, torch.int32, (B, max_pages), "page_table")
-    if q_offsets is not None:
-        _expect(q_offsets, torch.int32, (B + 1,), "q_offsets")
+        table = _dense(page_table, torch.int32, (B, max_pages), "page_table")
+    pages = None
     if prefix_len > 0:
         if prefix_pages is None:
             raise ValueError("prefix_pages: missing")
-        if prefix_pages.dtype != torch.int32:
-            raise TypeError("prefix_pages: expected torch.int32")
-        if prefix_pages.numel() * kv.page_size < prefix_len:
+        n = prefix_pages.numel()
+        if n * kv.page_size < prefix_len:
             raise ValueError("prefix_pages: fewer pages than prefix_len needs")
+        pages = _dense(prefix_pages, torch.int32, (n,), "prefix_pages")
     _check("moe_prefix_attention",
-           lib().moe_prefix_attention(ctypes.byref(kv), T, B, int(max_q), qp, qs,
-                                      _ptr(q_offsets), kc, vc,
-                                      _ptr(prefix_pages) if prefix_len > 0 else None,
-                                      int(prefix_len), _ptr(page_table), max_pages,
-                                      _ptr(kv_lens),
-                                      float(kv.head_dim ** -0.5 if scale is None else scale),
-                                      op, os_, _ptr(lse), ws.c_ptr, ws.nbytes, _stream(stream)))
+           _fn("moe_prefix_attention")(ctypes.byref(kv), T, B, max_q, qp, qs,
+                                       _dense(q_offsets, torch.int32, (B + 1,), "q_offsets"),
+                                       _dense(k_cache, dt, cache, "k_cache"),
+                                       _dense(v_cache, dt, cache, "v_cache"), pages, prefix_len,
+                                       table, max_pages,
+                                       _dense(kv_lens, torch.int32, (B,), "kv_lens"),
+                                       kv.head_dim ** -0.5 if scale is None else scale, op, os_,
+                                       _dense(lse, torch.float32, (T, hq), "lse"), ws.ptr,
+                                       ws.nbytes, _stream(stream)))
     return out, lse
 
 
