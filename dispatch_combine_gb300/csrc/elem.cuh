@@ -35,6 +35,53 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack2<DTYPE>(f[6], f[7]));
 }
 
+// ---- pairs of fp32 in one 64-bit register: one instruction for two elements
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// eight elements as four pairs
+template <int DTYPE>
+__device__ __forceinline__ void unpack8x2(const uint4 &v, uint64_t (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack2<DTYPE>(w[i]);
+    f[i] = pack_f32x2(p.x, p.y);
+  }
+}
+template <int DTYPE>
+__device__ __forceinline__ uint4 pack8x2(const uint64_t (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack_f32x2(f[i]);
+    w[i] = pack2<DTYPE>(p.x, p.y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <int DTYPE>
 __device__ __forceinline__ float load1(const void *p, int64_t i) {
   const uint32_t v = static_cast<const uint16_t *>(p)[i];

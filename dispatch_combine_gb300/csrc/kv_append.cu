@@ -30,18 +30,10 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const KvAppendArgs a) {
   const bool skip = slot < 0 || bad;
   if (bad && threadIdx.x == 0) set_status(a.status, kStatusBadId);
   const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < half; i += blockDim.x) {
-    // turns = position * inv_freq / 2 pi, its fraction in fp64: the product
-    // of a 31-bit and a 24-bit number rounds at 2^-53, so the fraction keeps
-    // at least 24 bits up to 2^31 positions
-    const double turns = static_cast<double>(a.positions[t]) * static_cast<double>(a.inv_freq[i]) *
-                         0.15915494309189535;
-    const float frac = static_cast<float>(turns - rint(turns));
-    sincospif(2.0f * frac, &s_sin[i], &s_cos[i]);
-  }
-  __syncthreads();
   const int64_t page = slot >> a.page_shift, in_page = slot & ((1 << a.page_shift) - 1);
-  for (int base = threadIdx.x; base < units; base += blockDim.x * kAppendUnroll) {
+  bool first = true;
+  // (every thread passes the loop once, for the barrier inside)
+  for (int base = threadIdx.x; first || base < units; base += blockDim.x * kAppendUnroll) {
     uint4 lo[kAppendUnroll], hi[kAppendUnroll];
     int head[kAppendUnroll], e0[kAppendUnroll], e1[kAppendUnroll];
 #pragma unroll
@@ -63,6 +55,19 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const KvAppendArgs a) {
         row = static_cast<const uint16_t *>(a.v) + t * a.v_stride + (head[j] - nq - a.hkv) * a.D;
       lo[j] = *reinterpret_cast<const uint4 *>(row + e0[j]);
       hi[j] = *reinterpret_cast<const uint4 *>(row + e1[j]);
+    }
+    if (first) {  // with the first units on their way
+      first = false;
+      for (int i = threadIdx.x; i < half; i += blockDim.x) {
+        // turns = position * inv_freq / 2 pi, its fraction in fp64: the product
+        // of a 31-bit and a 24-bit number rounds at 2^-53, so the fraction keeps
+        // at least 24 bits up to 2^31 positions
+        const double turns = static_cast<double>(a.positions[t]) * static_cast<double>(a.inv_freq[i]) *
+                             0.15915494309189535;
+        const float frac = static_cast<float>(turns - rint(turns));
+        sincospif(2.0f * frac, &s_sin[i], &s_cos[i]);
+      }
+      __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < kAppendUnroll; ++j) {
