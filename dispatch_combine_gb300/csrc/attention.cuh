@@ -19,18 +19,29 @@ namespace moe {
 
 // What the joining kernel needs of a sequence.
 struct SeqMeta {
-  int64_t cum;    // where its units start in the line
   int32_t unit;   // number of its first unit
   int32_t steps;  // per unit
 };
 
 // How the own rows of the sequences are cut (by either kernel).
 struct OwnPlan {
-  int tok;         // tokens of a unit
-  int step_keys;   // keys of a step
-  int step_cost, unit_cost;
-  int rows;        // rows of a slot (or of its half)
-  int64_t slot0;   // first row of its slots
+  int tok;        // tokens of a unit
+  int rows;       // rows of a slot (or of its half)
+  int64_t slot0;  // first row of its slots
+  int span0;      // its first unit's place in AttnArgs::span
+};
+// What a step of a unit costs there: constants of the kernel.
+struct SliceSteps {  // rows kernel
+  static constexpr int kKeys = 16, kUnitCost = 2;
+  static __device__ __forceinline__ int cost(int) { return 1; }
+  static __device__ __forceinline__ int steps_up(int x, int) { return x; }  // ceil(x / cost)
+};
+struct TileSteps {  // tiles kernel: a narrow tile 2, a wide one 3
+  static constexpr int kKeys = 128, kUnitCost = 1, kMostCost = 3;
+  static __device__ __forceinline__ int cost(int wide) { return 2 + wide; }
+  static __device__ __forceinline__ int steps_up(int x, int wide) {
+    return wide ? (x + 2) / 3 : (x + 1) / 2;
+  }
 };
 
 struct AttnArgs {
@@ -49,8 +60,10 @@ struct AttnArgs {
   int own_on, s_wide, s_box;
   OwnPlan own;
   int own_rows_kernel;               // the own rows are the rows kernel's
-  int64_t *pieces;                   // device: piece lengths (rows kernel; tiles kernel: gang CTAs, others)
   SeqMeta *meta;
+  // device: the first and the last worker of every unit (prefix units, then
+  // own units), written by those two
+  int2 *span;
   float *part_o, *part_lse;
 };
 
@@ -60,6 +73,7 @@ struct Seq {
 };
 
 // Sequence b with every value clamped into the buffers.
+template <class K>
 __device__ __forceinline__ Seq read_seq(const AttnArgs &g, int b, bool *bad_off, bool *bad) {
   const PrefixAttnArgs &a = g.a;
   Seq s = {0, 0, 0, 0, 0, 0};
@@ -78,11 +92,11 @@ __device__ __forceinline__ Seq read_seq(const AttnArgs &g, int b, bool *bad_off,
   const int len = a.kv_lens[b];
   if (len < 0 || len > cap) *bad = true;
   s.len = min(max(len, 0), cap);
-  s.steps = (s.len + g.own.step_keys - 1) / g.own.step_keys;
-  s.units = (s.nq + g.own.tok - 1) / g.own.tok * a.hkv;
-  s.cost = s.steps > 0
-               ? s.units * (static_cast<int64_t>(s.steps) * g.own.step_cost + g.own.unit_cost)
-               : 0;
+  s.steps = (s.len + K::kKeys - 1) / K::kKeys;
+  const int blocks = s.nq <= g.own.tok ? s.nq > 0 : (s.nq + g.own.tok - 1) / g.own.tok;
+  s.units = blocks * a.hkv;
+  s.cost = s.steps > 0 ? s.units * (static_cast<int64_t>(s.steps) * K::cost(g.s_wide) + K::kUnitCost)
+                       : 0;
   return s;
 }
 
@@ -107,7 +121,7 @@ struct ScanShared {
   int64_t warp_cost[THREADS / 32], before[THREADS];
   int warp_units[THREADS / 32], units[THREADS];
 };
-template <int THREADS>
+template <class K, int THREADS>
 __device__ __forceinline__ OwnScan scan_own(const AttnArgs &g, ScanShared<THREADS> &sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (g.a.B + THREADS - 1) / THREADS;
@@ -119,7 +133,7 @@ __device__ __forceinline__ OwnScan scan_own(const AttnArgs &g, ScanShared<THREAD
   bool bad_off = false, bad = false;
 #pragma unroll 1
   for (int b = r.b_lo; b < r.b_hi; ++b) {
-    const Seq s = read_seq(g, b, &bad_off, &bad);
+    const Seq s = read_seq<K>(g, b, &bad_off, &bad);
     my_cost += s.cost;
     my_units += s.units;
   }
@@ -158,15 +172,14 @@ __device__ __forceinline__ OwnScan scan_own(const AttnArgs &g, ScanShared<THREAD
   return r;
 }
 // The scan's values of each sequence for the joining kernel (one CTA).
+template <class K>
 __device__ __forceinline__ void write_meta(const AttnArgs &g, const OwnScan &r) {
   bool x = false, y = false;
-  int64_t cum = r.before;
   int unit = r.units_before;
 #pragma unroll 1
   for (int b = r.b_lo; b < r.b_hi; ++b) {
-    const Seq s = read_seq(g, b, &x, &y);
-    g.meta[b] = SeqMeta{cum, unit, r.drop ? 0 : s.steps};
-    cum += s.cost;
+    const Seq s = read_seq<K>(g, b, &x, &y);
+    g.meta[b] = SeqMeta{unit, r.drop ? 0 : s.steps};
     unit += s.units;
   }
   if (r.bad) set_status(g.a.status, kStatusBadId);
@@ -176,20 +189,29 @@ __device__ __forceinline__ void write_meta(const AttnArgs &g, const OwnScan &r) 
 struct Stretch {
   int head, tok0, ntok;  // key head, first token, tokens
   int lim0, kv_len;      // token i sees keys below min(kv_len, lim0 + i)
-  int s0, s1;            // steps
+  int s0, s1, n;         // steps [s0, s1) of n
   int64_t unit;          // its number among the units of its kind
   const int32_t *pages;
 };
 
-// steps [s0, s1) of a unit that starts at `start`, with n steps, in [lo, hi)
-__device__ __forceinline__ int step_at(int64_t ahead, int n, int cost) {
+// The unit's partial results: from which worker to which.
+__device__ __forceinline__ void mark_span(const AttnArgs &g, int64_t place, const Stretch &x,
+                                          int worker) {
+  if (x.s0 == 0) g.span[place].x = worker;
+  if (x.s1 == x.n) g.span[place].y = worker;
+}
+
+// the first of a unit's n steps at or past `ahead` of its start
+template <class K>
+__device__ __forceinline__ int step_at(int64_t ahead, int n, int wide) {
   if (ahead <= 0) return 0;
-  if (ahead >= static_cast<int64_t>(n) * cost) return n;
-  return (static_cast<int>(ahead) + cost - 1) / cost;
+  if (ahead >= static_cast<int64_t>(n) * K::cost(wide)) return n;
+  return K::steps_up(static_cast<int>(ahead), wide);
 }
 
 // Walks the own units in [lo, hi) of their line; a whole warp.  next() gives
 // one stretch at a time.
+template <class K>
 struct OwnWalk {
   int64_t lo, hi, cum0, batch, cum, start, unit_cost;
   int unit0, batch_units, base, un;
@@ -223,8 +245,9 @@ struct OwnWalk {
       if (j < n_units && start + j * unit_cost < hi) {
         const int at = j++;
         const int64_t from = start + at * unit_cost;
-        out->s0 = step_at(lo - from, steps, g.own.step_cost);
-        out->s1 = step_at(hi - from, steps, g.own.step_cost);
+        out->s0 = step_at<K>(lo - from, steps, g.s_wide);
+        out->s1 = step_at<K>(hi - from, steps, g.s_wide);
+        out->n = steps;
         if (out->s0 >= out->s1) continue;
         const int block = at / g.a.hkv;
         out->head = at - block * g.a.hkv;
@@ -248,7 +271,7 @@ struct OwnWalk {
         n_units = __shfl_sync(0xffffffffu, s.units, src);
         start = __shfl_sync(0xffffffffu, cum, src);
         unit = __shfl_sync(0xffffffffu, un, src);
-        unit_cost = static_cast<int64_t>(steps) * g.own.step_cost + g.own.unit_cost;
+        unit_cost = static_cast<int64_t>(steps) * K::cost(g.s_wide) + K::kUnitCost;
         j = lo <= start ? 0 : static_cast<int>(quotient(lo - start, unit_cost));
         continue;
       }
@@ -257,7 +280,7 @@ struct OwnWalk {
       unit0 += batch_units;
       if (base >= g.a.B || cum0 >= hi) return false;
       bool x = false, y = false;
-      s = read_seq(g, base + lane, &x, &y);
+      s = read_seq<K>(g, base + lane, &x, &y);
       cum = s.cost;
       un = s.units;
 #pragma unroll
@@ -295,13 +318,11 @@ struct Prob {
 };
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kTile = 128;      // keys per tile of the tiles kernel
-constexpr int kSlice = 16;      // keys per slice of the rows kernel
+constexpr int kTile = TileSteps::kKeys;    // keys per tile
+constexpr int kSlice = SliceSteps::kKeys;  // keys per slice
 constexpr int kMaxCtas = 160;   // grid limit of both (slots of partial results)
 constexpr int kRowWarps = 8;    // warps per CTA of the rows kernel
 constexpr int kMinSlices = 4;   // shortest piece of the rows kernel's line
-constexpr int kSliceUnit = 2;   // cost of starting a unit there, in slices
-constexpr int kWideCost = 3, kNarrowCost = 2, kTileUnit = 1;  // tiles kernel
 
 // prefix_attention_rows.cu, prefix_attention_tiles.cu
 cudaError_t launch_attention_rows(const AttnArgs &g, int dtype, int ctas, cudaStream_t s);

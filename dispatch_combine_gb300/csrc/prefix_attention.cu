@@ -31,6 +31,21 @@ struct Parts {
   }
 };
 
+// the row of a tile unit's token: in the half of a wide unit that holds it
+__device__ __forceinline__ int half_row(const AttnArgs &g, int in, int rows) {
+  return in < g.tpt ? in * g.G : rows + (in - g.tpt) * g.G;
+}
+
+// The workers of a unit, inside the slots whatever stands there (a tiles
+// kernel whose wait ran out leaves spans unwritten).
+__device__ __forceinline__ int2 span_of(const AttnArgs &g, int64_t place, bool rows_kernel) {
+  const int most = rows_kernel ? kMaxCtas * kRowWarps : kMaxCtas;
+  int2 w = g.span[place];
+  w.x = min(max(w.x, 0), most - 1);
+  w.y = min(max(w.y, w.x), most - 1);
+  return w;
+}
+
 // A warp per token and query head.
 template <int DTYPE, int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
@@ -50,6 +65,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
     if (lane == 0) s_ends[threadIdx.x >> 5] = n;
     __syncthreads();
     b = 0;
+#pragma unroll 1
     for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) b += s_ends[w];
   }
   const int h = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -57,57 +73,35 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
   const int kvh = h / g.G, hg = h - kvh * g.G;
   Parts pre = {0, 0, 0, 1, 0}, own = {0, 0, 0, 1, 0};
   if (g.r_prefix) {
-    const int64_t piece = g.pieces[0];
-    const int block = t / g.r_tok;
-    const int64_t u = static_cast<int64_t>(kvh) * g.r_blocks + block, start = u * g.r_pcost;
-    const int64_t w0 = quotient(start, piece), w1 = quotient(start + g.r_slices - 1, piece);
-    pre.first = (u + w0) * g.r_rows + (t - block * g.r_tok) * g.G + hg;
+    const int block = t / g.r_tok, u = kvh * g.r_blocks + block;
+    const int2 w = span_of(g, u, true);
     pre.step = g.r_rows;
-    pre.n = static_cast<int>(w1 - w0) + 1;
+    pre.first = static_cast<int64_t>(u + w.x) * g.r_rows + (t - block * g.r_tok) * g.G + hg;
+    pre.n = w.y - w.x + 1;
   } else if (g.p_on) {
     const int block = t / g.p_tok, in = t - block * g.p_tok;
     const int group = block / g.p_gang, member = block - group * g.p_gang;
-    const int64_t q = static_cast<int64_t>(kvh) * g.p_groups + group, start = q * g.p_tiles;
-    const int64_t g0 = quotient(start, g.p_piece), g1 = quotient(start + g.p_tiles - 1, g.p_piece);
-    pre.first = ((q + g0) * g.p_gang + member) * 2 * g.p_rows +
-                (g.p_wide ? in / g.tpt * g.p_rows : 0) + in % g.tpt * g.G + hg;
+    const int64_t q = static_cast<int64_t>(kvh) * g.p_groups + group;
+    const int2 w = span_of(g, q * g.p_gang + member, false);
     pre.step = static_cast<int64_t>(g.p_gang) * 2 * g.p_rows;
-    pre.n = static_cast<int>(g1 - g0) + 1;
     pre.halves = g.p_wide ? 1 : 2;
     pre.half_step = g.p_rows;
+    pre.first = (q + w.x) * pre.step + member * 2 * g.p_rows + half_row(g, in, g.p_rows) + hg;
+    pre.n = w.y - w.x + 1;
   }
   if ((g.own_rows_kernel || g.own_on) && b < a.B) {
     const SeqMeta m = g.meta[b];
     const int place = t - (a.q_offsets ? a.q_offsets[b] : b);
     if (place >= 0 && place < a.max_q && m.steps > 0) {
       const int block = place / g.own.tok, in = place - block * g.own.tok;
-      const int j = block * a.hkv + kvh;
-      const int64_t span = static_cast<int64_t>(m.steps - 1) * g.own.step_cost;
-      const int64_t start =
-          m.cum + j * (span + g.own.step_cost + g.own.unit_cost);
-      int64_t w0, w1;
-      if (g.own_rows_kernel) {
-        const int64_t piece = g.pieces[0];
-        w0 = quotient(g.r_ptotal + start, piece);
-        w1 = quotient(g.r_ptotal + start + span, piece);
-        own.first = in * g.G + hg;
-        own.step = g.own.rows;
-      } else {
-        const int64_t ganged = g.p_on ? g.p_gangs * g.p_gang : 0;
-        const int64_t len0 = g.pieces[1], len1 = g.pieces[2];
-        auto worker = [&](int64_t pos) {
-          return pos < ganged * len0 ? quotient(pos, len0)
-                                     : ganged + quotient(pos - ganged * len0, len1);
-        };
-        w0 = worker(start);
-        w1 = worker(start + span);
-        own.first = (g.s_wide ? in / g.tpt * g.own.rows : 0) + in % g.tpt * g.G + hg;
-        own.step = 2 * g.own.rows;
-        own.halves = g.s_wide ? 1 : 2;
-        own.half_step = g.own.rows;
-      }
-      own.first += g.own.slot0 + (m.unit + j + w0) * own.step;
-      own.n = static_cast<int>(w1 - w0) + 1;
+      const int u = m.unit + block * a.hkv + kvh;
+      const int2 w = span_of(g, g.own.span0 + u, g.own_rows_kernel);
+      own.halves = g.own_rows_kernel || g.s_wide ? 1 : 2;
+      own.half_step = g.own.rows;
+      own.step = g.own_rows_kernel ? g.own.rows : 2 * g.own.rows;
+      own.first = g.own.slot0 + static_cast<int64_t>(u + w.x) * own.step +
+                  (g.own_rows_kernel ? in * g.G : half_row(g, in, g.own.rows)) + hg;
+      own.n = w.y - w.x + 1;
     }
   }
   const int np = pre.count(), parts = np + own.count();
@@ -127,7 +121,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
     const int64_t mine = i < parts ? row_of(i) : 0;
     const float wgt = i < parts ? ex2(g.part_lse[mine] - ref) : 0.0f;
     const int m = min(32, parts - base);
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < m; ++k) {
       const float wk = __shfl_sync(0xffffffffu, wgt, k);
       const int64_t rk = __shfl_sync(0xffffffffu, mine, k);
@@ -169,7 +163,7 @@ constexpr int kPrefixRows = 32, kOwnRows = 64;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Scratch {
-  size_t meta, lse, o, bytes;
+  size_t span, lse, o, bytes;
 };
 
 // own_rows: whether sequences can have rows of their own
@@ -193,7 +187,7 @@ Scratch plan(AttnArgs &g, int T, int B, int max_q, int hq, int hkv, int D, int p
   g.r_rows = g.r_tok * G;
   g.r_blocks = (T + g.r_tok - 1) / g.r_tok;
   g.r_slices = g.r_prefix ? (prefix_len + kSlice - 1) / kSlice : 0;
-  g.r_pcost = g.r_slices + kSliceUnit;
+  g.r_pcost = g.r_slices + SliceSteps::kUnitCost;
   g.r_ptotal = g.r_prefix ? static_cast<int64_t>(hkv) * g.r_blocks * g.r_pcost : 0;
   // tiles kernel
   g.p_wide = T > g.tpt;
@@ -223,31 +217,30 @@ Scratch plan(AttnArgs &g, int T, int B, int max_q, int hq, int hkv, int D, int p
   g.s_box = std::min(g.tpt, nq);
   if (g.own_rows_kernel) {
     g.own.tok = std::min(g.r_tok, nq);
-    g.own.step_keys = kSlice;
-    g.own.step_cost = 1;
-    g.own.unit_cost = kSliceUnit;
     g.own.rows = g.own.tok * G;
   } else {
     g.own.tok = g.s_wide ? 2 * g.tpt : g.tpt;
-    g.own.step_keys = kTile;
-    g.own.step_cost = g.s_wide ? kWideCost : kNarrowCost;
-    g.own.unit_cost = kTileUnit;
     g.own.rows = g.s_box * G;
   }
-  int64_t rows = 0;
-  if (g.r_prefix)
+  int64_t rows = 0, units = 0;
+  if (g.r_prefix) {
+    units = static_cast<int64_t>(hkv) * g.r_blocks;
     rows = (static_cast<int64_t>(hkv) * g.r_blocks + kMaxCtas * kRowWarps) * g.r_rows;
-  else if (g.p_on)  // (hkv * groups + gangs) * gang slots, whatever the grid
-    rows = (static_cast<int64_t>(hkv) * (g.p_blocks + 16) + kMaxCtas) * 2 * g.p_rows;
+  } else if (g.p_on) {  // (hkv * groups + gangs) * gang slots, whatever the grid
+    units = static_cast<int64_t>(hkv) * (g.p_blocks + 16);
+    rows = (units + kMaxCtas) * 2 * g.p_rows;
+  }
   g.own.slot0 = rows;
+  g.own.span0 = static_cast<int>(units);
   if (own) {
-    const int64_t units = static_cast<int64_t>(hkv) * (B + T / g.own.tok);
-    rows += g.own_rows_kernel ? (units + kMaxCtas * kRowWarps) * g.own.rows
-                              : (units + kMaxCtas) * 2 * g.own.rows;
+    const int64_t more = static_cast<int64_t>(hkv) * (B + T / g.own.tok);
+    units += more;
+    rows += g.own_rows_kernel ? (more + kMaxCtas * kRowWarps) * g.own.rows
+                              : (more + kMaxCtas) * 2 * g.own.rows;
   }
   Scratch s;
-  s.meta = 256;
-  s.lse = up256(s.meta + sizeof(SeqMeta) * static_cast<size_t>(B));
+  s.span = up256(sizeof(SeqMeta) * static_cast<size_t>(B));
+  s.lse = up256(s.span + sizeof(int2) * static_cast<size_t>(units));
   s.o = up256(s.lse + 4 * static_cast<size_t>(rows));
   s.bytes = up256(s.o + 4 * static_cast<size_t>(rows) * D);
   return s;
@@ -278,8 +271,8 @@ cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, int dtype, cudaStre
   const int ctas = std::min(num_sms(), kMaxCtas);
   const Scratch sc =
       plan(g, a.T, a.B, a.max_q, a.hq, a.hkv, a.D, a.prefix_len, a.max_pages > 0, ctas);
-  g.pieces = reinterpret_cast<int64_t *>(a.scratch);
-  g.meta = reinterpret_cast<SeqMeta *>(a.scratch + sc.meta);
+  g.meta = reinterpret_cast<SeqMeta *>(a.scratch);
+  g.span = reinterpret_cast<int2 *>(a.scratch + sc.span);
   g.part_lse = reinterpret_cast<float *>(a.scratch + sc.lse);
   g.part_o = reinterpret_cast<float *>(a.scratch + sc.o);
   if (g.r_on) {

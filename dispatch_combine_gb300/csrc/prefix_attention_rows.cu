@@ -132,9 +132,6 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < C::STAGES - 1; ++i) load(x.s0 + i);
-
   float o[MT][D / 8][4], mx[MT][2], l[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -149,7 +146,8 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
   const float lag = Prob<DTYPE>::kLag / sl2;
   const int all_seen = min(x.kv_len, x.lim0);  // keys that every token sees
 #pragma unroll 1
-  for (int s = x.s0; s < x.s1; ++s) {
+  for (int s = x.s0 - (C::STAGES - 1); s < x.s1; ++s) {
+    if (s >= x.s0) {  // the first passes only fill the ring
     cp_async_wait<C::STAGES - 2>();
     __syncwarp();
     const int stage = (s - x.s0) % C::STAGES;
@@ -242,6 +240,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
       }
     }
     __syncwarp();  // the stage of the last slice is free again
+    }
     load(s + C::STAGES - 1);
   }
   cp_async_wait<0>();
@@ -275,35 +274,33 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) attention_rows_kernel(const
   __shared__ ScanShared<kRowWarps * 32> scan;
   const int warp = threadIdx.x >> 5;
   OwnScan own = {};
-  if (g.own_rows_kernel) own = scan_own(g, scan);
+  if (g.own_rows_kernel) own = scan_own<SliceSteps>(g, scan);
   const int64_t total = g.r_ptotal + own.total;
   const int64_t piece = max(quotient(total + gridDim.x * kRowWarps - 1, gridDim.x * kRowWarps),
                             static_cast<int64_t>(kMinSlices));
-  if (blockIdx.x == 0) {
-    if (g.own_rows_kernel) write_meta(g, own);
-    if (threadIdx.x == 0) g.pieces[0] = piece;
-  }
+  if (blockIdx.x == 0 && g.own_rows_kernel) write_meta<SliceSteps>(g, own);
   // consecutive pieces on different SMs
-  const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-  const int64_t lo = worker * piece, hi = min(lo + piece, total);
+  const int worker = warp * gridDim.x + blockIdx.x;
+  const int64_t lo = static_cast<int64_t>(worker) * piece, hi = min(lo + piece, total);
   if (lo >= total) return;
   const uint32_t ring = smem_u32(smem) + warp * C::WARP_BYTES;
   const bool any_own = own.total > 0 && hi > g.r_ptotal;
-  OwnWalk walk;
+  OwnWalk<SliceSteps> walk;
   if (any_own) walk.begin(g, scan, max(lo - g.r_ptotal, int64_t{0}), hi - g.r_ptotal);
   int64_t u = lo < g.r_ptotal ? quotient(lo, g.r_pcost) : 0;
   bool in_prefix = lo < g.r_ptotal;
   while (true) {
     Stretch x;
-    int64_t slot;
+    int64_t slot, place;
     if (in_prefix) {
       if (u * g.r_pcost >= min(hi, g.r_ptotal)) {
         in_prefix = false;
         continue;
       }
       const int64_t at = u++;
-      x.s0 = step_at(lo - at * g.r_pcost, g.r_slices, 1);
-      x.s1 = step_at(hi - at * g.r_pcost, g.r_slices, 1);
+      x.n = g.r_slices;
+      x.s0 = step_at<SliceSteps>(lo - at * g.r_pcost, x.n, 0);
+      x.s1 = step_at<SliceSteps>(hi - at * g.r_pcost, x.n, 0);
       if (x.s0 >= x.s1) continue;
       x.head = static_cast<int>(quotient(at, g.r_blocks));
       x.tok0 = static_cast<int>(at - static_cast<int64_t>(x.head) * g.r_blocks) * g.r_tok;
@@ -311,10 +308,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) attention_rows_kernel(const
       x.lim0 = x.kv_len = g.a.prefix_len;
       x.pages = g.a.prefix_pages;
       slot = (at + worker) * g.r_rows;
+      place = at;
     } else {
       if (!any_own || !walk.next(g, &x)) break;
       slot = g.own.slot0 + (x.unit + worker) * g.own.rows;
+      place = g.own.span0 + x.unit;
     }
+    if ((threadIdx.x & 31) == 0) mark_span(g, place, x, worker);
     attend<DTYPE, D, MT>(g, x, slot, ring);
   }
 }

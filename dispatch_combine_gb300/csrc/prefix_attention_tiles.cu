@@ -251,13 +251,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // prefix), then a piece [lo, hi) of the own units' line.  The CTAs outside
   // the gangs take more of that line: all are to end at the same time.
   OwnScan own = {};
-  if (g.own_on) own = scan_own(g, scan);
+  if (g.own_on) own = scan_own<TileSteps>(g, scan);
   const int ganged = g.p_on ? g.p_gangs * g.p_gang : 0, cta = blockIdx.x;
   const int others = gridDim.x - ganged;
-  const int64_t p_time = g.p_on ? g.p_piece * (g.p_wide ? kWideCost : kNarrowCost) : 0;
+  const int64_t p_time = g.p_on ? g.p_piece * TileSteps::cost(g.p_wide) : 0;
   int64_t own_ganged = 0, own_other = 1;
   if (own.total > 0) {
-    const int64_t least = kWideCost;
+    const int64_t least = TileSteps::kMostCost;
     if (own.total <= others * p_time) {
       own_other = max(quotient(own.total + others - 1, others), least);
     } else {
@@ -266,13 +266,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (others == 0) own_other = least;
     }
   }
-  if (blockIdx.x == 0) {
-    if (g.own_on) write_meta(g, own);
-    if (threadIdx.x == 0) {
-      g.pieces[1] = own_ganged;
-      g.pieces[2] = own_other;
-    }
-  }
+  if (blockIdx.x == 0 && g.own_on) write_meta<TileSteps>(g, own);
   const int64_t lo = cta < ganged ? cta * own_ganged
                                   : ganged * own_ganged + (cta - ganged) * own_other;
   const int64_t hi = min(lo + (cta < ganged ? own_ganged : own_other), own.total);
@@ -303,17 +297,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                  : 0;
     int64_t p_at = in_gang ? p_lo : 0;
     const bool any_own = own.total > 0 && lo < hi;
-    OwnWalk walk;
+    OwnWalk<TileSteps> walk;
     if (any_own) walk.begin(g, scan, lo, hi);
     while (ok) {
       Stretch x;
-      int64_t slot;
+      int64_t slot, place;
       const bool is_own = p_at >= p_hi;
       if (!is_own) {
         const int64_t q = quotient(p_at, g.p_tiles);  // key head and group
         x.head = static_cast<int>(quotient(q, g.p_groups));
         x.s0 = static_cast<int>(p_at - q * g.p_tiles);
         x.s1 = static_cast<int>(min(static_cast<int64_t>(g.p_tiles), x.s0 + (p_hi - p_at)));
+        x.n = g.p_tiles;
         p_at += x.s1 - x.s0;
         const int block = static_cast<int>(q - static_cast<int64_t>(x.head) * g.p_groups) *
                               g.p_gang + member;
@@ -323,10 +318,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         x.lim0 = x.kv_len = a.prefix_len;
         x.pages = a.prefix_pages;
         slot = ((q + gang) * g.p_gang + member) * 2 * g.p_rows;
+        place = q * g.p_gang + member;
       } else {
         if (!any_own || !walk.next(g, &x)) break;
         slot = g.own.slot0 + (x.unit + cta) * 2 * g.own.rows;
+        place = g.own.span0 + x.unit;
       }
+      if (lane == 0) mark_span(g, place, x, is_own ? cta : gang);
       const int head = x.head, tok0 = x.tok0, kv_len = x.kv_len, t0 = x.s0, t1 = x.s1;
       const int wide = is_own ? g.s_wide : g.p_wide;
       const int32_t *pages = x.pages;
