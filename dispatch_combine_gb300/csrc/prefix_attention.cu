@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
   const int np = pre.count(), parts = np + own.count();
   auto row_of = [&](int i) { return i < np ? pre.row(i) : own.row(i - np); };
   float top = -INFINITY;
-#pragma unroll 1
+#pragma unroll 2
   for (int i = lane; i < parts; i += 32) top = fmaxf(top, g.part_lse[row_of(i)]);
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -118,26 +118,28 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
 #pragma unroll 1
   for (int base = 0; base < parts; base += 32) {
     const int i = base + lane;
-    const int64_t mine = i < parts ? row_of(i) : 0;
+    const int64_t mine = row_of(min(i, parts - 1));
     const float wgt = i < parts ? ex2(g.part_lse[mine] - ref) : 0.0f;
     const int m = min(32, parts - base);
-#pragma unroll 2
-    for (int k = 0; k < m; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, wgt, k);
-      const int64_t rk = __shfl_sync(0xffffffffu, mine, k);
-      l += wk;
-      if (wk == 0.0f) continue;  // an empty part has no row
-      const float *src = g.part_o + rk * D + lane * E;
-      if (E == 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(src);
-        o[0] = fmaf(wk, x.x, o[0]);
-        o[1] = fmaf(wk, x.y, o[1]);
-        o[E - 2] = fmaf(wk, x.z, o[E - 2]);
-        o[E - 1] = fmaf(wk, x.w, o[E - 1]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2 *>(src);
-        o[0] = fmaf(wk, x.x, o[0]);
-        o[1] = fmaf(wk, x.y, o[1]);
+    // eight rows on their way at a time; a part with weight 0 may have no row
+    // (whatever lies there does not count), nor do those past the end
+#pragma unroll 1
+    for (int k = 0; k < m; k += 8) {
+      float x[8][E];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float *src = g.part_o + __shfl_sync(0xffffffffu, mine, k + c) * D + lane * E;
+        if (E == 4)
+          *reinterpret_cast<float4 *>(x[c]) = *reinterpret_cast<const float4 *>(src);
+        else
+          *reinterpret_cast<float2 *>(x[c]) = *reinterpret_cast<const float2 *>(src);
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float wk = __shfl_sync(0xffffffffu, wgt, k + c);
+        l += wk;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = wk == 0.0f ? o[e] : fmaf(wk, x[c][e], o[e]);
       }
     }
   }
