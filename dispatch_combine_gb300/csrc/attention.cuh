@@ -322,7 +322,7 @@ constexpr int kTile = TileSteps::kKeys;    // keys per tile
 constexpr int kSlice = SliceSteps::kKeys;  // keys per slice
 constexpr int kMaxCtas = 160;   // grid limit of both (slots of partial results)
 constexpr int kRowWarps = 8;    // warps per CTA of the rows kernel
-constexpr int kMinSlices = 4;   // shortest piece of the rows kernel's line
+constexpr int kMinSlices = 2;   // shortest piece of the rows kernel's line
 
 // prefix_attention_rows.cu, prefix_attention_tiles.cu
 cudaError_t launch_attention_rows(const AttnArgs &g, int dtype, int ctas, cudaStream_t s);

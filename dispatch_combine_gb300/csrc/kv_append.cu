@@ -10,7 +10,10 @@
 namespace moe {
 namespace {
 
-constexpr int kAppendUnroll = 2;
+// units per thread whose loads are in flight together: a prefill step of 16384
+// tokens (64 + 8 heads of 128) takes 144 us with one, 124 with two, 109 with
+// four (671 MB: 6.1 TB/s, 0.91 of the measured copy bandwidth)
+constexpr int kAppendUnroll = 4;
 
 // One CTA per token.  Its work is cut into units of 16 elements (two 16-byte
 // vectors): for the half style, vector c of the first half of the rotated
@@ -18,7 +21,7 @@ constexpr int kAppendUnroll = 2;
 // not rotated, two neighbouring vectors.  Units are numbered through the
 // token's query heads, key heads, value heads.
 template <int DTYPE>
-__global__ void __launch_bounds__(512) kv_append_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(512, 2) kv_append_kernel(const KvAppendArgs a) {
   pdl_begin();
   __shared__ float s_cos[64], s_sin[64];
   const int t = blockIdx.x;

@@ -140,12 +140,6 @@ __device__ __forceinline__ void bar_commit(uint32_t bar) {  // when the MMAs so 
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
 }
-// The bounded wait, out of line: its code is long, and it reads the global
-// timer, which takes about a microsecond.
-__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                       uint32_t *status, uint64_t limit_ns) {
-  return mbar_wait_bounded(bar, parity, abort, status, limit_ns);
-}
 // What a wait needs when it becomes long.
 struct WaitCtx {
   uint32_t base;  // shared address of the barriers
@@ -154,14 +148,22 @@ struct WaitCtx {
   uint32_t *status;
   uint64_t limit_ns;
 };
-// Whole warp: true for all lanes when the phase completed, false for all when
-// some lane gave up.
-__device__ __forceinline__ bool wait_bar(const WaitCtx &c, uint32_t bar, uint32_t parity) {
+// The wait proper, out of line (a dozen places wait, and code that does not
+// stay in the instruction cache costs more than the call): polls for as long
+// as several tiles take, then by the clock (the global timer takes about a
+// microsecond to read).
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, const WaitCtx &c) {
 #pragma unroll 1
   for (int i = 0; i < 2048; ++i)
     if (__all_sync(0xffffffffu, bar_test(bar, parity))) return true;
-  return __all_sync(0xffffffffu, wait_long(c.bars + (bar - c.base) / 8, parity, c.abort, c.status,
-                                           c.limit_ns));
+  return __all_sync(0xffffffffu, mbar_wait_bounded(c.bars + (bar - c.base) / 8, parity, c.abort,
+                                                   c.status, c.limit_ns));
+}
+// Whole warp: true for all lanes when the phase completed, false for all when
+// some lane gave up.
+__device__ __forceinline__ bool wait_bar(const WaitCtx &c, uint32_t bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, bar_test(bar, parity))) return true;
+  return wait_long(bar, parity, c);
 }
 // Time-bounded wait that ignores the abort flag (to drain after an abort).
 __device__ __noinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
@@ -284,6 +286,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   if (warp == 8) {
     // ---------------- loader: walks the line, fetches Q, K and V ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(g.p_on ? &tmQp : &tmQs);
+    }
     const int ppt = max(1, kTile >> a.page_shift);  // pages per tile
     const int page_rows = min(1 << a.page_shift, kTile);
     uint32_t issued[2] = {0, 0}, nseg = 0, q_use[2] = {0, 0};  // issued: K and V tiles
@@ -328,6 +335,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int head = x.head, tok0 = x.tok0, kv_len = x.kv_len, t0 = x.s0, t1 = x.s1;
       const int wide = is_own ? g.s_wide : g.p_wide;
       const int32_t *pages = x.pages;
+      auto page_at = [&](int t) {
+        int p = -1;
+        const int first = static_cast<int>((static_cast<int64_t>(t) * kTile) >> a.page_shift);
+        const int last = (kv_len - 1) >> a.page_shift;
+        if (t < t1 && lane < ppt && first + lane <= last) {
+          p = pages[first + lane];
+          if (p < 0 || p >= a.num_pages) {
+            set_status(a.status, kStatusBadId);
+            p = 0;
+          }
+        }
+        return p;
+      };
+      int page = page_at(t0);  // on its way while the segment is published
       // publish the segment, then fetch its queries and tiles
       const uint32_t r = nseg % kDescs;
       ok = wait_bar(wc, BAR(d_empty, r), ((nseg / kDescs) & 1u) ^ 1u);
@@ -354,20 +375,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       if (!ok) break;
-      auto page_at = [&](int t) {
-        int p = -1;
-        const int first = static_cast<int>((static_cast<int64_t>(t) * kTile) >> a.page_shift);
-        const int last = (kv_len - 1) >> a.page_shift;
-        if (t < t1 && lane < ppt && first + lane <= last) {
-          p = pages[first + lane];
-          if (p < 0 || p >= a.num_pages) {
-            set_status(a.status, kStatusBadId);
-            p = 0;
-          }
-        }
-        return p;
-      };
-      int page = page_at(t0);
 #pragma unroll 1
       for (int t = t0; t < t1; ++t) {
         const int next = page_at(t + 1);
