@@ -35,6 +35,15 @@ struct AttnCfg {
   static constexpr int BLK = kTile * 128;           // 128 rows x 64 elements
   static constexpr int TILE_BYTES = (D / 64) * BLK;  // a K, V or Q tile
   static constexpr int STAGES = D == 128 ? 2 : 4;
+  // Columns of TMEM: scores 128 a group, accumulators D a group.  At D = 128
+  // that is all, and the probabilities lie over the scores; at D = 64 they have
+  // columns of their own, so that the next scores are computed while the
+  // exponentials of these are taken (256 queries over 131072 rows: 610 ->
+  // 540 us).
+  static constexpr bool APART = D == 64;
+  static constexpr int T_P = APART ? 256 : 0;
+  static constexpr int T_P_STEP = APART ? 64 : 128;
+  static constexpr int T_O = APART ? 384 : 256;
   static constexpr int K_OFF = 2 * TILE_BYTES;
   static constexpr int V_OFF = K_OFF + STAGES * TILE_BYTES;
   static constexpr int BAR_OFF = V_OFF + STAGES * TILE_BYTES;
@@ -185,8 +194,9 @@ struct Bars {
   uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2];  // scores of a group are in TMEM
+  uint64_t s_read[2];  // and in its threads' registers (APART)
   uint64_t p_lo[2], p_hi[2];  // its probabilities are: keys 0-63, 64-127
-  uint64_t o_full[2];  // its segment's accumulator is complete
+  uint64_t o_full[2];  // its accumulator is: at the segment's end (APART: after every step)
   uint64_t d_full[kDescs], d_empty[kDescs];
   uint64_t drain[2];
   Segment seg[kDescs];
@@ -237,6 +247,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&bar.q_full[h], 1);
       mbar_init(&bar.q_empty[h], 2);
       mbar_init(&bar.s_full[h], 1);
+      mbar_init(&bar.s_read[h], 4);
       mbar_init(&bar.p_lo[h], 4);
       mbar_init(&bar.p_hi[h], 4);
       mbar_init(&bar.o_full[h], 1);
@@ -442,7 +453,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint64_t desc_k = sw128_kmajor_desc(smem_u32(smem + C::K_OFF));
     const uint64_t desc_v = sw128_nmajor_desc(smem_u32(smem + C::V_OFF), C::BLK);
     const int w = warp - 9;
-    const uint32_t t_s = tmem_base + w * 128, t_o = tmem_base + 256 + w * 128;
+    const uint32_t t_s = tmem_base + w * 128, t_p = tmem_base + C::T_P + w * C::T_P_STEP;
+    const uint32_t t_o = tmem_base + C::T_O + w * D;
     uint32_t nseg = 0, step = 0, p_use = 0, k_tile = 0, v_tile = 0;
     uint32_t q_par = 0;  // a bit per query buffer
     bool ok = true, any = false;
@@ -513,6 +525,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
 #pragma unroll 1
       for (int i = 0; ok && i < n; ++i) {
+        if (C::APART && i + 1 < n) {  // the next scores, once these are read
+          if (!wide) skip_k();
+          ok = ok && wait_bar(wc, BAR(s_read, w), p_use & 1u);
+          scores(i + 2 == n);
+        }
         if (!wide && (i || i0)) skip_v();
         const uint32_t st = v_tile % C::STAGES, v_par = (v_tile / C::STAGES) & 1u;
         const uint32_t p_par = p_use & 1u;
@@ -526,7 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            mma_ts(t_o, t_s + k * 8, vd + k * (16 * 128 / 16), kIdescPV, (i || k) ? 1u : 0u);
+            mma_ts(t_o, t_p + k * 8, vd + k * (16 * 128 / 16), kIdescPV, (i || k) ? 1u : 0u);
         }
         __syncwarp();
         ok = wait_bar(wc, BAR(p_hi, w), p_par);
@@ -535,14 +552,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int k = kTile / 32; k < kTile / 16; ++k)
-            mma_ts(t_o, t_s + k * 8, vd + k * (16 * 128 / 16), kIdescPV, 1u);
+            mma_ts(t_o, t_p + k * 8, vd + k * (16 * 128 / 16), kIdescPV, 1u);
           bar_commit(BAR(v_empty, st));
-          if (i == n - 1) bar_commit(BAR(o_full, w));
+          if (C::APART || i == n - 1) bar_commit(BAR(o_full, w));
         }
         __syncwarp();
         ++p_use;
         ++v_tile;
-        if (i + 1 < n) {
+        if (!C::APART && i + 1 < n) {
           if (!wide) skip_k();
           scores(i + 2 == n);
         }
@@ -561,7 +578,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int w = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t ts = tmem_base + lane_base + w * 128, to = tmem_base + lane_base + 256 + w * 128;
+    const uint32_t ts = tmem_base + lane_base + w * 128;
+    const uint32_t tp = tmem_base + lane_base + C::T_P + w * C::T_P_STEP;
+    const uint32_t to = tmem_base + lane_base + C::T_O + w * D;
     constexpr float kOff = Prob<DTYPE>::kOff;
     const float sl2 = a.scale * kLog2e;
     const float lag = Prob<DTYPE>::kLag / sl2;
@@ -609,9 +628,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int d = 0; d < kBlocks; ++d) st_shared_v4(v0 + d * C::BLK + c * 16, 0, 0, 0, 0);
           fence_proxy_async_smem();
         }
+        // APART: the product of the last step must have read its probabilities
+        // before these overwrite them
+        auto last_product = [&]() {
+          if (!C::APART || i == 0) return true;
+          ok = wait_bar(wc, BAR(o_full, w), o_use & 1u);
+          ++o_use;
+          tc_fence_after();
+          return ok;
+        };
         if (rare(!warp_live)) {
           tc_fence_before();
           __syncwarp();
+          if (C::APART && lane == 0) bar_arrive(BAR(s_read, w));
+          if (!last_product()) break;
           if (lane == 0) {
             bar_arrive(BAR(p_lo, w));
             bar_arrive(BAR(p_hi, w));
@@ -626,6 +656,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_regs_fence(v[c]);
+        if (C::APART) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(BAR(s_read, w));
+        }
         if (rare(masked)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -642,6 +677,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             asm("max.f32 %0, %0, %1, %2;" : "+f"(tops[c]) : "f"(x), "f"(y));
           }
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        if (!last_product()) break;
         const bool moves = top > m + lag;
         if (rare(__any_sync(0xffffffffu, moves))) {
           const float m1 = moves ? top : m;
@@ -680,7 +716,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             sums[j & 3] = add_f32x2(sums[j & 3], pack_f32x2(e.x, e.y));
             p[j] = pack2<DTYPE>(e.x, e.y);
           }
-          tmem_st_32x32b_x16(ts + c * 16, p);
+          tmem_st_32x32b_x16(tp + c * 16, p);
           if (c == 1 || c == 3) {  // the MMA issuer starts on the first half
             tmem_st_wait();
             tc_fence_before();
