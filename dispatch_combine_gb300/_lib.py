@@ -193,12 +193,13 @@ def _ptr(t):
 # The current stream's handle without building a Stream object (a few
 # microseconds less per call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -688,9 +689,10 @@ _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16}
 
 
 def _dtype(t):
-    if t not in _DTYPES:
+    code = _DTYPES.get(t)
+    if code is None:
         raise TypeError(f"expected torch.bfloat16 or torch.float16, got {t}")
-    return _DTYPES[t]
+    return code
 
 
 def _refuse_rows(t, dtype, shape, name):
@@ -704,17 +706,27 @@ def _refuse_rows(t, dtype, shape, name):
 
 
 def _rows(t, dtype, shape, name):
-    """Address and row stride of a tensor whose rows (its first dimension) may
-    be strided, each row dense."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda:
-        st = t.stride()
-        width = shape[-1]
-        if len(shape) == 3:
-            if (st[1] == width or shape[1] == 1) and (st[2] == 1 or width == 1):
-                width *= shape[1]
-                return t.data_ptr(), st[0] if shape[0] > 1 else width
-        elif st[1] == 1 or width == 1:
-            return t.data_ptr(), st[0] if shape[0] > 1 else width
+    """Address and row stride of a [T, d] tensor whose rows may be strided,
+    each row dense."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+            row, one = t.stride()
+            if one == 1:
+                return t.data_ptr(), row if shape[0] > 1 else shape[1]
+    except AttributeError:
+        pass
+    _refuse_rows(t, dtype, shape, name)
+
+
+def _heads(t, dtype, shape, name):
+    """The same of a [T, heads, D] tensor: the heads of a token are dense."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+            row, head, one = t.stride()
+            if one == 1 and (head == shape[2] or shape[1] == 1):
+                return t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2]
+    except AttributeError:
+        pass
     _refuse_rows(t, dtype, shape, name)
 
 
@@ -722,16 +734,18 @@ def _dense(t, dtype, shape, name):
     """Address of a dense tensor; None for None."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda \
-            and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _ptr(t)
     _expect(t, dtype, shape, name)
 
 
 @functools.lru_cache(maxsize=256)
 def _norm_struct(T, d, kind, dtype, eps, weight_offset):
-    return ctypes.byref(MoeNorm(T, d, kind, dtype, eps, weight_offset))
+    return ctypes.byref(MoeNorm(T, d, int(kind), dtype, float(eps), float(weight_offset)))
 
 
 def _fn(name):
@@ -744,12 +758,13 @@ def moe_norm_in(x, weight=None, bias=None, kind=MOE_NORM_RMS, eps=1e-6, weight_o
     if x.dim() != 2:
         raise ValueError("x: expected [T, d]")
     shape, dt = x.shape, x.dtype
-    n = _norm_struct(shape[0], shape[1], int(kind), _dtype(dt), float(eps), float(weight_offset))
+    T, d = shape
+    n = _norm_struct(T, d, kind, _dtype(dt), eps, weight_offset)
     if out is None:
         out = torch.empty(shape, dtype=dt, device=x.device)
     xp, xs = _rows(x, dt, shape, "x")
     op, os_ = _rows(out, dt, shape, "out")
-    vec = shape[1:]
+    vec = (d,)
     _check("moe_norm_in",
            _fn("moe_norm_in")(n, xp, xs, _dense(weight, dt, vec, "weight"),
                               _dense(bias, dt, vec, "bias"), op, os_, _stream(stream)))
@@ -769,7 +784,7 @@ def moe_norm_out(f, x, post_weight=None, post_bias=None, gate=None, residual_sca
         raise ValueError("x: expected [T, d]")
     shape, dt = x.shape, x.dtype
     T, d = shape
-    n = _norm_struct(T, d, int(kind), _dtype(dt), float(eps), float(weight_offset))
+    n = _norm_struct(T, d, kind, _dtype(dt), eps, weight_offset)
     if post_norm is None:
         post_norm = post_weight is not None
     if next_norm is None:
@@ -796,7 +811,7 @@ def moe_norm_out(f, x, post_weight=None, post_bias=None, gate=None, residual_sca
     fp, fs = _rows(f, dt, shape, "f")
     xp, xs = _rows(x, dt, shape, "x")
     xo, xos = _rows(x_out, dt, shape, "x_out")
-    vec = shape[1:]
+    vec = (d,)
     _check("moe_norm_out",
            _fn("moe_norm_out")(n, fp, fs, xp, xs, 1 if post_norm else 0,
                                _dense(post_weight, dt, vec, "post_weight"),
@@ -827,13 +842,13 @@ def moe_kv_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cac
     qp, qs, qo, qos = None, 0, None, 0
     if q is not None:
         shape = (T, kv.num_q_heads, D)
-        qp, qs = _rows(q, dt, shape, "q")
+        qp, qs = _heads(q, dt, shape, "q")
         if q_out is None:
             q_out = torch.empty(shape, dtype=dt, device=q.device)
-        qo, qos = _rows(q_out, dt, shape, "q_out")
+        qo, qos = _heads(q_out, dt, shape, "q_out")
     shape = (T, hkv, D)
-    kp, ks = _rows(k, dt, shape, "k")
-    vp, vs = _rows(v, dt, shape, "v")
+    kp, ks = _heads(k, dt, shape, "k")
+    vp, vs = _heads(v, dt, shape, "v")
     rot, fp, pp = 0, None, None
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
@@ -873,8 +888,8 @@ def moe_prefix_attention(kv: MoeKv, q, k_cache, v_cache, prefix_pages, prefix_le
         out = torch.empty(shape, dtype=dt, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-    qp, qs = _rows(q, dt, shape, "q")
-    op, os_ = _rows(out, dt, shape, "out")
+    qp, qs = _heads(q, dt, shape, "q")
+    op, os_ = _heads(out, dt, shape, "out")
     cache = (kv.num_pages, kv.num_kv_heads, kv.page_size, kv.head_dim)
     max_pages, table = 0, None
     if page_table is not None:
