@@ -57,6 +57,8 @@ struct AttnArgs {
   int p_on, p_wide, p_tok, p_blocks, p_tiles, p_rows, p_box;
   int p_gang, p_groups, p_gangs;     // CTAs of a gang, token blocks / gang, gangs
   int64_t p_piece;                   // tiles of a gang's piece
+  int share;                         // the rows kernel does the own rows beside it: the tiles
+                                     // kernel works out how many of its gangs to use
   int own_on, s_wide, s_box;
   OwnPlan own;
   int own_rows_kernel;               // the own rows are the rows kernel's
@@ -326,7 +328,6 @@ constexpr int kMinSlices = 2;   // shortest piece of the rows kernel's line
 
 // prefix_attention_rows.cu, prefix_attention_tiles.cu
 cudaError_t launch_attention_rows(const AttnArgs &g, int dtype, int ctas, cudaStream_t s);
-cudaError_t launch_attention_tiles(const AttnArgs &g, int dtype, int ctas, bool after_rows,
-                                   cudaStream_t s);
+cudaError_t launch_attention_tiles(const AttnArgs &g, int dtype, int ctas, cudaStream_t s);
 
 }  // namespace moe

@@ -8,6 +8,12 @@
 // once and stays in registers through both statistics, so the kernel moves
 // each input and output row exactly once; everything is fp32 until the one
 // rounding of each output.
+//
+// Bound by HBM where there are many rows: 16384 x 7168 bf16 moves 470 MB in
+// 73 us (6.4 TB/s, 0.94 of the measured copy bandwidth) for one input and one
+// output, 940 MB in 180 us (5.2 TB/s) for two and two, where the arithmetic of
+// two norms comes near the issue rate.  A row per CTA, so that rows in flight,
+// not barriers, set the rate; with few rows the launch is the time (3 us).
 #include "elem.cuh"
 #include "kernels.h"
 

@@ -7,7 +7,10 @@
 // (cp.async, the next slices always in flight), and keeps queries, scores,
 // probabilities and accumulators in registers (mma.sync m16n8k16, which a
 // few rows fill better than a 128-row tensor-memory tile).  Warps never wait
-// for one another; eight of them per SM keep up to 128 KB in flight.
+// for one another; eight of them per SM keep up to 128 KB in flight.  Bound by
+// HBM: 64 sequences of up to 8192 rows (1.23 GB of cache in 190 us) run at 0.95
+// of the measured copy bandwidth, 256 of up to 512 (287 MB) in 64 us with the
+// join, one token over 131072 shared rows (537 MB) in 96 us.
 //
 // Layouts.  K and V slices are copied as they lie in a page (16 rows of one
 // head, contiguous), 16-byte chunk c of row r at chunk c ^ 4 (r & 1) for K and
@@ -20,12 +23,15 @@
 namespace moe {
 namespace {
 
-template <int D>
+// WARPS per CTA: 8 when the kernel has the GPU for itself; 2 beside the tiles
+// kernel, where it starts on the SMs that one leaves free and the CTAs that
+// wait take over the others as they come free.
+template <int D, int WARPS>
 struct RowCfg {
-  static constexpr int SLICE = kSlice * D * 2;         // bytes of K or of V
-  static constexpr int STAGES = D == 128 ? 3 : 6;      // 24 KB per warp
+  static constexpr int SLICE = kSlice * D * 2;     // bytes of K or of V
+  static constexpr int STAGES = D == 128 ? 3 : 6;  // 24 KB per warp
   static constexpr int WARP_BYTES = STAGES * 2 * SLICE;
-  static constexpr int SMEM_BYTES = kRowWarps * WARP_BYTES;
+  static constexpr int SMEM_BYTES = WARPS * WARP_BYTES;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -70,10 +76,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // One stretch, by one warp.  `slot`: first row of its partial result.
-template <int DTYPE, int D, int MT>
+template <int DTYPE, int D, int MT, int WARPS>
 __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int64_t slot,
                                        uint32_t ring) {
-  using C = RowCfg<D>;
+  using C = RowCfg<D, WARPS>;
   const PrefixAttnArgs &a = g.a;
   const int lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
   const int rows = x.ntok * g.G;
@@ -266,23 +272,38 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
     }
 }
 
-template <int DTYPE, int D, int MT>
-__global__ void __launch_bounds__(kRowWarps * 32, 1) attention_rows_kernel(const AttnArgs g) {
-  pdl_begin();
-  using C = RowCfg<D>;
+template <int DTYPE, int D, int MT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, kRowWarps / WARPS)
+    attention_rows_kernel(const AttnArgs g, const int beside) {
+  // Beside the tiles kernel of the same call, which has waited for everything
+  // before the call and shares nothing with this one: only the last CTA waits
+  // for it, at its end, so that whoever waits for this kernel has waited for
+  // both.
+  if (beside)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  else
+    pdl_begin();
+  using C = RowCfg<D, WARPS>;
+  auto leave = [&]() {
+    if (beside && blockIdx.x == gridDim.x - 1)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ ScanShared<kRowWarps * 32> scan;
+  __shared__ ScanShared<WARPS * 32> scan;
   const int warp = threadIdx.x >> 5;
   OwnScan own = {};
   if (g.own_rows_kernel) own = scan_own<SliceSteps>(g, scan);
   const int64_t total = g.r_ptotal + own.total;
-  const int64_t piece = max(quotient(total + gridDim.x * kRowWarps - 1, gridDim.x * kRowWarps),
+  const int64_t piece = max(quotient(total + gridDim.x * WARPS - 1, gridDim.x * WARPS),
                             static_cast<int64_t>(kMinSlices));
   if (blockIdx.x == 0 && g.own_rows_kernel) write_meta<SliceSteps>(g, own);
   // consecutive pieces on different SMs
   const int worker = warp * gridDim.x + blockIdx.x;
   const int64_t lo = static_cast<int64_t>(worker) * piece, hi = min(lo + piece, total);
-  if (lo >= total) return;
+  if (lo >= total) {
+    leave();
+    return;
+  }
   const uint32_t ring = smem_u32(smem) + warp * C::WARP_BYTES;
   const bool any_own = own.total > 0 && hi > g.r_ptotal;
   OwnWalk<SliceSteps> walk;
@@ -315,32 +336,37 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) attention_rows_kernel(const
       place = g.own.span0 + x.unit;
     }
     if ((threadIdx.x & 31) == 0) mark_span(g, place, x, worker);
-    attend<DTYPE, D, MT>(g, x, slot, ring);
+    attend<DTYPE, D, MT, WARPS>(g, x, slot, ring);
   }
+  leave();
 }
 
-template <int DTYPE, int D, int MT>
+template <int DTYPE, int D, int MT, int WARPS>
 cudaError_t run(const AttnArgs &g, int ctas, cudaStream_t s) {
-  using C = RowCfg<D>;
+  using C = RowCfg<D, WARPS>;
+  auto kernel = attention_rows_kernel<DTYPE, D, MT, WARPS>;
   const cudaError_t err =
-      cudaFuncSetAttribute(attention_rows_kernel<DTYPE, D, MT>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (err != cudaSuccess) return err;
-  MOE_LAUNCH_PDL(attention_rows_kernel<DTYPE, D, MT>, ctas, kRowWarps * 32, C::SMEM_BYTES, s, g);
+  MOE_LAUNCH_PDL(kernel, ctas * kRowWarps / WARPS, WARPS * 32, C::SMEM_BYTES, s, g, g.share);
   return cudaGetLastError();
 }
 
-template <int DTYPE>
+template <int DTYPE, int D>
 cudaError_t run_d(const AttnArgs &g, int ctas, cudaStream_t s) {
-  if (g.a.D == 64) return g.r_mt == 1 ? run<DTYPE, 64, 1>(g, ctas, s) : run<DTYPE, 64, 2>(g, ctas, s);
-  return g.r_mt == 1 ? run<DTYPE, 128, 1>(g, ctas, s) : run<DTYPE, 128, 2>(g, ctas, s);
+  if (g.share) return g.r_mt == 1 ? run<DTYPE, D, 1, 2>(g, ctas, s) : run<DTYPE, D, 2, 2>(g, ctas, s);
+  return g.r_mt == 1 ? run<DTYPE, D, 1, kRowWarps>(g, ctas, s)
+                     : run<DTYPE, D, 2, kRowWarps>(g, ctas, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_rows(const AttnArgs &g, int dtype, int ctas, cudaStream_t s) {
-  return dtype == MOE_DTYPE_BF16 ? run_d<MOE_DTYPE_BF16>(g, ctas, s)
-                                 : run_d<MOE_DTYPE_FP16>(g, ctas, s);
+  if (dtype == MOE_DTYPE_BF16)
+    return g.a.D == 64 ? run_d<MOE_DTYPE_BF16, 64>(g, ctas, s)
+                       : run_d<MOE_DTYPE_BF16, 128>(g, ctas, s);
+  return g.a.D == 64 ? run_d<MOE_DTYPE_FP16, 64>(g, ctas, s)
+                     : run_d<MOE_DTYPE_FP16, 128>(g, ctas, s);
 }
 
 }  // namespace moe

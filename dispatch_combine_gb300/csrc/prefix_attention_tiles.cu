@@ -16,8 +16,10 @@
 // find it in L2.  The own rows of the sequences follow, cut so that all CTAs
 // end together.
 //
-// Bounds: the tensor cores (4 D flop per score).  A tile pair of a wide unit
-// is 32 products of 128 x 128 x 16 per SM at 64 cycles.
+// Bound by the tensor cores (4 D flop per score): a tile of a wide unit is 32
+// products of 128 x 128 x 16 per SM at 64 cycles.  256 queries x 64 heads of
+// 128 over 131072 rows (1.10 PFLOP) take 755 us, 0.75 of the measured bf16
+// peak; the MMAs alone would take 570, the softmax alone 545.
 #include <algorithm>
 #include <cstddef>
 #include <mutex>
@@ -183,6 +185,35 @@ __device__ __noinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint64_t
   }
 }
 
+// How many gangs to use when the rows kernel has `slices` slices of own rows to
+// read beside: the number that lets both end first (the warp tries 32 at a
+// time).  A gang's tiles cost a fixed time each; an SM left to the rows kernel
+// is counted with 55 GB/s of cache beside the tiles, all SMs with 6.4 TB/s, and
+// what is left when the tiles are done is read by all.  45, 55, 65 and 90 GB/s
+// gave 51.7, 51.7, 57.7 and 55.7 us for 64 sequences (64 + 8 heads of 128,
+// prefix 8192, own rows up to 1024), 229, 228, 240 and 241 us for 256 (32768,
+// 512), and 131, 120, 120 and 120 us for 64 (32 + 8 heads, 2048, 4096); 0.75
+// and 1.25 times the tile time change them by 1 %.
+template <int D>
+__device__ __forceinline__ int shared_gangs(const AttnArgs &g, int64_t slices, int ctas) {
+  const float tile_us = (D == 128 ? 1.75f : 1.25f) * (g.p_wide ? 1.0f : 0.6f), start_us = 9.0f;
+  const float bytes = static_cast<float>(slices) * (64.0f * D);
+  const float tiles = static_cast<float>(g.a.hkv) * g.p_groups * g.p_tiles;
+  float best = INFINITY;
+  int use = g.p_gangs;
+  for (int k = 1 + (threadIdx.x & 31); k <= g.p_gangs; k += 32) {
+    const float t = ceilf(tiles / k) * tile_us + start_us;
+    const float rate = fminf((ctas - k * g.p_gang) * 55e3f, 6.4e6f);
+    const float end = t + fmaxf(bytes - t * rate, 0.0f) * (1.0f / 6.4e6f);
+    if (end <= best) {
+      best = end;
+      use = k;
+    }
+  }
+  const unsigned first = __reduce_min_sync(0xffffffffu, __float_as_uint(best));
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(best) == first ? use : 1);
+}
+
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
@@ -209,15 +240,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV,
                             const __grid_constant__ CUtensorMap tmQp,
-                            const __grid_constant__ CUtensorMap tmQs, const AttnArgs g,
-                           const int after_rows) {
-  // After the rows kernel of the same call, which has waited for everything
-  // before the call and shares nothing with this one: wait for it at the end
-  // only, so that whoever waits for this kernel has waited for both.
-  if (after_rows)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  else
-    pdl_begin();
+                            const __grid_constant__ CUtensorMap tmQs, const AttnArgs g) {
+  pdl_begin();
   using C = AttnCfg<D>;
   constexpr int kBlocks = D / 64;
   extern __shared__ uint8_t smem_raw[];
@@ -264,10 +288,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // prefix), then a piece [lo, hi) of the own units' line.  The CTAs outside
   // the gangs take more of that line: all are to end at the same time.
   OwnScan own = {};
-  if (g.own_on) own = scan_own<TileSteps>(g, scan);
-  const int ganged = g.p_on ? g.p_gangs * g.p_gang : 0, cta = blockIdx.x;
+  int gangs = g.p_gangs;
+  int64_t p_piece = g.p_piece;
+  if (g.own_on) {
+    own = scan_own<TileSteps>(g, scan);
+  } else if (g.share) {
+    // the rows kernel gets the SMs of the gangs that are not used
+    const int64_t slices = scan_own<SliceSteps>(g, scan).total;
+    gangs = shared_gangs<D>(g, slices, gridDim.x);
+    p_piece = quotient(static_cast<int64_t>(a.hkv) * g.p_groups * g.p_tiles + gangs - 1, gangs);
+  }
+  const int ganged = g.p_on ? gangs * g.p_gang : 0, cta = blockIdx.x;
   const int others = gridDim.x - ganged;
-  const int64_t p_time = g.p_on ? g.p_piece * TileSteps::cost(g.p_wide) : 0;
+  const int64_t p_time = g.p_on ? p_piece * TileSteps::cost(g.p_wide) : 0;
   int64_t own_ganged = 0, own_other = 1;
   if (own.total > 0) {
     const int64_t least = TileSteps::kMostCost;
@@ -284,10 +317,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                   : ganged * own_ganged + (cta - ganged) * own_other;
   const int64_t hi = min(lo + (cta < ganged ? own_ganged : own_other), own.total);
   const bool in_gang = cta < ganged;
-  if (!in_gang && lo >= own.total) {  // uniform across the CTA
-    if (after_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
+  if (!in_gang && lo >= own.total) return;  // uniform across the CTA
   __syncthreads();
   if (warp == 9) tmem_alloc(&bar.tmem, 512);
   tc_fence_before();
@@ -309,8 +339,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // the gang's stretch of the prefix line (key head, group of blocks, tile):
     // this member has one block of each group
     const int gang = in_gang ? cta / g.p_gang : 0, member = cta - gang * g.p_gang;
-    const int64_t p_lo = gang * g.p_piece;
-    const int64_t p_hi = in_gang ? min(p_lo + g.p_piece, static_cast<int64_t>(a.hkv) *
+    const int64_t p_lo = gang * p_piece;
+    const int64_t p_hi = in_gang ? min(p_lo + p_piece, static_cast<int64_t>(a.hkv) *
                                                              g.p_groups * g.p_tiles)
                                  : 0;
     int64_t p_at = in_gang ? p_lo : 0;
@@ -770,7 +800,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem_base, 512);
-  if (after_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
 #undef BAR
 }
 
@@ -817,7 +846,7 @@ bool attn_tmap(CUtensorMap *map, int dtype, const void *base, uint64_t n0, uint6
 }
 
 template <int DTYPE, int D>
-cudaError_t run(const AttnArgs &g, int ctas, bool after_rows, cudaStream_t s) {
+cudaError_t run(const AttnArgs &g, int ctas, cudaStream_t s) {
   using C = AttnCfg<D>;
   const PrefixAttnArgs &a = g.a;
   CUtensorMap tmK, tmV, tmQp, tmQs;
@@ -835,19 +864,18 @@ cudaError_t run(const AttnArgs &g, int ctas, bool after_rows, cudaStream_t s) {
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (err != cudaSuccess) return err;
   MOE_LAUNCH_PDL(attention_tiles_kernel<DTYPE, D>, ctas, kAttnThreads, C::SMEM_BYTES, s, tmK, tmV,
-                 tmQp, tmQs, g, after_rows ? 1 : 0);
+                 tmQp, tmQs, g);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attention_tiles(const AttnArgs &g, int dtype, int ctas, bool after_rows,
-                                   cudaStream_t s) {
+cudaError_t launch_attention_tiles(const AttnArgs &g, int dtype, int ctas, cudaStream_t s) {
   if (dtype == MOE_DTYPE_BF16)
-    return g.a.D == 64 ? run<MOE_DTYPE_BF16, 64>(g, ctas, after_rows, s)
-                       : run<MOE_DTYPE_BF16, 128>(g, ctas, after_rows, s);
-  return g.a.D == 64 ? run<MOE_DTYPE_FP16, 64>(g, ctas, after_rows, s)
-                     : run<MOE_DTYPE_FP16, 128>(g, ctas, after_rows, s);
+    return g.a.D == 64 ? run<MOE_DTYPE_BF16, 64>(g, ctas, s)
+                       : run<MOE_DTYPE_BF16, 128>(g, ctas, s);
+  return g.a.D == 64 ? run<MOE_DTYPE_FP16, 64>(g, ctas, s)
+                     : run<MOE_DTYPE_FP16, 128>(g, ctas, s);
 }
 
 }  // namespace moe
