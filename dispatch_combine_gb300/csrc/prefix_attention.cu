@@ -54,7 +54,10 @@ __device__ __forceinline__ int2 span_of(const AttnArgs &g, int64_t place, bool r
 // fill the GPU).
 template <int DTYPE, int D, int W>
 __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
-  pdl_begin();
+  // A kernel of the same call that ran before has waited for everything before
+  // the call, so the call's inputs can be read ahead of this one's own wait.
+  const bool alone = !g.r_on && !g.t_on;
+  if (alone) pdl_begin();
   constexpr int E = D / 32;
   constexpr int kBatch = W > 1 ? 8 : 4;  // with many rows the other warps hide a row's way
   const PrefixAttnArgs &a = g.a;
@@ -74,6 +77,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
 #pragma unroll 1
     for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) b += s_ends[w];
   }
+  if (!alone) pdl_begin();
   const int h0 = (blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)) / W;
   const int wi = (threadIdx.x >> 5) % W;
   if (W == 1 && h0 >= a.hq) return;
@@ -120,9 +124,29 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
   }
   const int np = pre.count(), parts = np + own.count();
   auto row_of = [&](int i) { return i < np ? pre.row(i) : own.row(i - np); };
-  float top = -INFINITY;
+  // kBatch rows on their way at a time, the first of them before the maximum is
+  // known; a part with weight 0 may have no row, and whatever lies there does
+  // not count
+  float x[kBatch][E];
+  int here = min(32, parts);
+  int64_t mine = row_of(min(lane, max(parts, 1) - 1));
+  auto fetch = [&](int k) {
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c) {
+      const float *src = g.part_o + __shfl_sync(0xffffffffu, mine, k + c) * D + lane * E;
+      if (k + c < here) {
+        if (E == 4)
+          *reinterpret_cast<float4 *>(x[c]) = *reinterpret_cast<const float4 *>(src);
+        else
+          *reinterpret_cast<float2 *>(x[c]) = *reinterpret_cast<const float2 *>(src);
+      }
+    }
+  };
+  float lse = lane < parts ? g.part_lse[mine] : -INFINITY;
+  if (kBatch * wi < here) fetch(kBatch * wi);
+  float top = lse;
 #pragma unroll 2
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, g.part_lse[row_of(i)]);
+  for (int i = lane + 32; i < parts; i += 32) top = fmaxf(top, g.part_lse[row_of(i)]);
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   const float ref = top == -INFINITY ? 0.0f : top;
@@ -130,34 +154,26 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
 #pragma unroll 1
-  for (int base = 0; base < parts; base += 32) {
-    const int i = base + lane;
-    const int64_t mine = row_of(min(i, parts - 1));
-    const float wgt = i < parts ? ex2(g.part_lse[mine] - ref) : 0.0f;
-    const int here = min(32, parts - base);
-    // kBatch rows on their way at a time; a part with weight 0 may have no
-    // row, and whatever lies there does not count
+  for (int base = 0; base < parts;) {
+    const float wgt = ex2(lse - ref);  // 0 past the end
 #pragma unroll 1
-    for (int k = kBatch * wi; k < here; k += kBatch * W) {
-      float x[kBatch][E];
+    for (int k = kBatch * wi; k < here;) {
 #pragma unroll
       for (int c = 0; c < kBatch; ++c) {
-        const float *src = g.part_o + __shfl_sync(0xffffffffu, mine, k + c) * D + lane * E;
-        if (k + c < here) {
-          if (E == 4)
-            *reinterpret_cast<float4 *>(x[c]) = *reinterpret_cast<const float4 *>(src);
-          else
-            *reinterpret_cast<float2 *>(x[c]) = *reinterpret_cast<const float2 *>(src);
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kBatch; ++c) {
-        const float wk = __shfl_sync(0xffffffffu, wgt, k + c);  // 0 past the end
+        const float wk = __shfl_sync(0xffffffffu, wgt, k + c);
         l += wk;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = wk == 0.0f ? o[e] : fmaf(wk, x[c][e], o[e]);
       }
+      k += kBatch * W;
+      if (k < here) fetch(k);
     }
+    base += 32;
+    if (base >= parts) break;
+    here = min(32, parts - base);
+    mine = row_of(min(base + lane, parts - 1));
+    lse = base + lane < parts ? g.part_lse[mine] : -INFINITY;
+    if (kBatch * wi < here) fetch(kBatch * wi);
   }
   if (W > 1) {
     __shared__ float s_o[8][E + 1][32];
