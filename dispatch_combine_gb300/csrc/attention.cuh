@@ -31,6 +31,9 @@ struct OwnPlan {
   int span0;      // its first unit's place in AttnArgs::span
 };
 // What a step of a unit costs there: constants of the kernel.
+constexpr int kMaxCtas = 160;   // grid limit of both (slots of partial results)
+constexpr int kRowWarps = 8;    // warps per CTA of the rows kernel
+
 struct SliceSteps {  // rows kernel
   static constexpr int kKeys = 16, kUnitCost = 2;
   static __device__ __forceinline__ int cost(int) { return 1; }
@@ -173,6 +176,57 @@ __device__ __forceinline__ OwnScan scan_own(const AttnArgs &g, ScanShared<THREAD
   __syncthreads();
   return r;
 }
+
+// What each kernel gets when the rows kernel has `slices` slices of own rows to
+// read beside the prefix's tiles; a whole warp.  Both ends are estimated for
+// every number of gangs (the warp tries 32 at a time) from measured rates, and
+// the first is taken: a gang's tiles cost a fixed time each, the rows run at
+// sm_rate per SM left to them up to the HBM's rate, and either stay on those
+// SMs or, cut into pieces for all SMs, go on everywhere once the tiles are done
+// (at the price of one more start and a part of a piece: 64 sequences with one
+// own row each over a prefix of 1024 took 26.2 us without it, 22.8 with it).
+//   sm_rate 60, 70, 80 GB/s at D = 128: 64 sequences, prefix 8192, own rows up
+// to 1024: 53.8, 51.7, 49.7 us; 64, 2048 and 4096: 115.7, 115.6, 120.2; 128,
+// 8192 and 512: 67.8, 65.8, 65.3.  45, 55, 65 at D = 64: 37 drafts, 20000 and
+// 777: 52.6, 52.7, 61.8; 100, 4099 and 2000: 47.6, 49.5, 52.9.  Without
+// rows_us0: 37 drafts, 4099 and 777: 33.4 instead of 29.1.
+struct ShareOut {
+  int gangs, workers;
+};
+template <int D>
+__device__ __forceinline__ ShareOut share_out(const AttnArgs &g, int64_t slices, int ctas) {
+  const float tile_us = (D == 128 ? 1.75f : 1.25f) * (g.p_wide ? 1.0f : 0.6f), tiles_us0 = 9.0f;
+  const float sm_rate = D == 128 ? 70e3f : 45e3f, hbm_rate = 6.4e6f, rows_us0 = 5.0f;  // per us
+  const float bytes = static_cast<float>(slices) * (64.0f * D);
+  const float tiles = static_cast<float>(g.a.hkv) * g.p_groups * g.p_tiles;
+  const float tail = 3.5f + 0.25f * bytes / (ctas * sm_rate);
+  struct Ends {
+    float tiles, rows, rows_all;
+  };
+  auto ends = [&](int k) {
+    const float t = tiles_us0 + ceilf(tiles / k) * tile_us;
+    const float rate = fminf((ctas - k * g.p_gang) * sm_rate, hbm_rate);
+    return Ends{t, rate > 0.0f ? rows_us0 + bytes / rate : INFINITY,
+                t + fmaxf(bytes - (t - rows_us0) * rate, 0.0f) / hbm_rate + tail};
+  };
+  float best = INFINITY;
+  int use = 1;
+  for (int k = 1 + (threadIdx.x & 31); k <= g.p_gangs; k += 32) {
+    const Ends e = ends(k);
+    // where the rows take longest any way, the fewer tiles in a row the better
+    const float cost = fmaxf(e.tiles, fminf(e.rows, e.rows_all)) + e.tiles * (1.0f / 16);
+    if (cost < best) {
+      best = cost;
+      use = k;
+    }
+  }
+  const unsigned first = __reduce_min_sync(0xffffffffu, __float_as_uint(best));  // best > 0
+  use = __reduce_min_sync(0xffffffffu, __float_as_uint(best) == first ? use : g.p_gangs);
+  const Ends e = ends(use);
+  const int left = e.rows <= e.rows_all ? ctas - use * g.p_gang : ctas;
+  return {use, left * kRowWarps};
+}
+
 // The scan's values of each sequence for the joining kernel (one CTA).
 template <class K>
 __device__ __forceinline__ void write_meta(const AttnArgs &g, const OwnScan &r) {
@@ -322,8 +376,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int kTile = TileSteps::kKeys;    // keys per tile
 constexpr int kSlice = SliceSteps::kKeys;  // keys per slice
-constexpr int kMaxCtas = 160;   // grid limit of both (slots of partial results)
-constexpr int kRowWarps = 8;    // warps per CTA of the rows kernel
 constexpr int kMinSlices = 2;   // shortest piece of the rows kernel's line
 
 // prefix_attention_rows.cu, prefix_attention_tiles.cu

@@ -14,7 +14,7 @@
 // side by side: the tiles kernel uses as many SMs as lets both end together
 // (it reads the lengths on the device), and the rows kernel, launched behind it
 // without waiting for it, starts on the others (64 sequences, prefix 8192, own
-// rows up to 1024: 63.5 us one after the other, 51.7 so; 256, 32768 and 512: 247
+// rows up to 1024: 63.5 us one after the other, 51.5 so; 256, 32768 and 512: 247
 // and 228).
 #include <algorithm>
 

@@ -294,13 +294,15 @@ __global__ void __launch_bounds__(WARPS * 32, kRowWarps / WARPS)
   OwnScan own = {};
   if (g.own_rows_kernel) own = scan_own<SliceSteps>(g, scan);
   const int64_t total = g.r_ptotal + own.total;
-  const int64_t piece = max(quotient(total + gridDim.x * WARPS - 1, gridDim.x * WARPS),
+  int ctas = gridDim.x;
+  if (beside) ctas = share_out<D>(g, own.total, ctas * WARPS / kRowWarps).workers / WARPS;
+  const int64_t piece = max(quotient(total + ctas * WARPS - 1, ctas * WARPS),
                             static_cast<int64_t>(kMinSlices));
   if (blockIdx.x == 0 && g.own_rows_kernel) write_meta<SliceSteps>(g, own);
   // consecutive pieces on different SMs
-  const int worker = warp * gridDim.x + blockIdx.x;
+  const int worker = warp * ctas + blockIdx.x;
   const int64_t lo = static_cast<int64_t>(worker) * piece, hi = min(lo + piece, total);
-  if (lo >= total) {
+  if (lo >= total || static_cast<int>(blockIdx.x) >= ctas) {
     leave();
     return;
   }

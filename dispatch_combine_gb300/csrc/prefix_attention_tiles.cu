@@ -185,35 +185,6 @@ __device__ __noinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint64_t
   }
 }
 
-// How many gangs to use when the rows kernel has `slices` slices of own rows to
-// read beside: the number that lets both end first (the warp tries 32 at a
-// time).  A gang's tiles cost a fixed time each; an SM left to the rows kernel
-// is counted with 55 GB/s of cache beside the tiles, all SMs with 6.4 TB/s, and
-// what is left when the tiles are done is read by all.  45, 55, 65 and 90 GB/s
-// gave 51.7, 51.7, 57.7 and 55.7 us for 64 sequences (64 + 8 heads of 128,
-// prefix 8192, own rows up to 1024), 229, 228, 240 and 241 us for 256 (32768,
-// 512), and 131, 120, 120 and 120 us for 64 (32 + 8 heads, 2048, 4096); 0.75
-// and 1.25 times the tile time change them by 1 %.
-template <int D>
-__device__ __forceinline__ int shared_gangs(const AttnArgs &g, int64_t slices, int ctas) {
-  const float tile_us = (D == 128 ? 1.75f : 1.25f) * (g.p_wide ? 1.0f : 0.6f), start_us = 9.0f;
-  const float bytes = static_cast<float>(slices) * (64.0f * D);
-  const float tiles = static_cast<float>(g.a.hkv) * g.p_groups * g.p_tiles;
-  float best = INFINITY;
-  int use = g.p_gangs;
-  for (int k = 1 + (threadIdx.x & 31); k <= g.p_gangs; k += 32) {
-    const float t = ceilf(tiles / k) * tile_us + start_us;
-    const float rate = fminf((ctas - k * g.p_gang) * 55e3f, 6.4e6f);
-    const float end = t + fmaxf(bytes - t * rate, 0.0f) * (1.0f / 6.4e6f);
-    if (end <= best) {
-      best = end;
-      use = k;
-    }
-  }
-  const unsigned first = __reduce_min_sync(0xffffffffu, __float_as_uint(best));
-  return __reduce_max_sync(0xffffffffu, __float_as_uint(best) == first ? use : 1);
-}
-
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
@@ -242,6 +213,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             const __grid_constant__ CUtensorMap tmQp,
                             const __grid_constant__ CUtensorMap tmQs, const AttnArgs g) {
   pdl_begin();
+  if (!g.own_on && static_cast<int>(blockIdx.x) >= g.p_gangs * g.p_gang) return;
   using C = AttnCfg<D>;
   constexpr int kBlocks = D / 64;
   extern __shared__ uint8_t smem_raw[];
@@ -295,7 +267,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   } else if (g.share) {
     // the rows kernel gets the SMs of the gangs that are not used
     const int64_t slices = scan_own<SliceSteps>(g, scan).total;
-    gangs = shared_gangs<D>(g, slices, gridDim.x);
+    gangs = share_out<D>(g, slices, gridDim.x).gangs;
     p_piece = quotient(static_cast<int64_t>(a.hkv) * g.p_groups * g.p_tiles + gangs - 1, gangs);
   }
   const int ganged = g.p_on ? gangs * g.p_gang : 0, cta = blockIdx.x;
