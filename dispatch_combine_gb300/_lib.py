@@ -798,7 +798,8 @@ def moe_norm_out(f, x, post_weight=None, post_bias=None, gate=None, residual_sca
         elif gshape == (d,):
             gate_kind, gp = MOE_GATE_CHANNEL, _dense(gate, dt, gshape, "gate")
         elif gshape in ((T,), (T, 1)):
-            gate_kind, gp = MOE_GATE_TOKEN, _dense(gate.contiguous(), dt, gshape, "gate")
+            gate = gate.contiguous()  # a copy is kept until the launch
+            gate_kind, gp = MOE_GATE_TOKEN, _dense(gate, dt, gshape, "gate")
         else:
             raise ValueError(f"gate: expected [{d}], [{T}], [{T}, 1] or [{T}, {d}], got {gshape}")
     if x_out is None:

@@ -185,3 +185,31 @@ def test_binding_refuses_on_the_host():
         moe.moe_kv_append(k_, q, k, k, i32, i32, None, cache, cache)
     with pytest.raises(ValueError):
         moe.moe_prefix_attention(k_, q[:, :4], cache, cache, i32, 0, None, i32, None)
+
+
+def test_a_strided_token_gate_lives_until_the_call(monkeypatch):
+    """Its dense copy must not be freed before the outputs are allocated: they
+    could get its memory."""
+    import weakref
+
+    from dispatch_combine_gb300 import _lib
+
+    seen = {}
+
+    def dense(t, dtype, shape, name):
+        if t is not None and name == "gate":
+            assert t.is_contiguous()
+            seen["gate"] = weakref.ref(t)
+        return None if t is None else t.data_ptr()
+
+    def call(*args):
+        seen["alive"] = seen["gate"]() is not None
+        return 0
+
+    monkeypatch.setattr(_lib, "_dense", dense)
+    monkeypatch.setattr(_lib, "_rows", lambda t, dtype, shape, name: (t.data_ptr(), t.stride(0)))
+    monkeypatch.setattr(_lib, "_fn", lambda name: call)
+    monkeypatch.setattr(_lib, "_stream", lambda s: 0)
+    f = torch.zeros(32, 8, dtype=torch.bfloat16)
+    _lib.moe_norm_out(f, f, gate=torch.zeros(32, 4, dtype=torch.bfloat16)[:, 1])
+    assert seen["alive"]
