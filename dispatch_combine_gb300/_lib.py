@@ -760,10 +760,12 @@ def moe_norm_in(x, weight=None, bias=None, kind=MOE_NORM_RMS, eps=1e-6, weight_o
     shape, dt = x.shape, x.dtype
     T, d = shape
     n = _norm_struct(T, d, kind, _dtype(dt), eps, weight_offset)
+    xp, xs = _rows(x, dt, shape, "x")
     if out is None:
         out = torch.empty(shape, dtype=dt, device=x.device)
-    xp, xs = _rows(x, dt, shape, "x")
-    op, os_ = _rows(out, dt, shape, "out")
+        op, os_ = out.data_ptr(), d
+    else:
+        op, os_ = _rows(out, dt, shape, "out")
     vec = (d,)
     _check("moe_norm_in",
            _fn("moe_norm_in")(n, xp, xs, _dense(weight, dt, vec, "weight"),
@@ -802,16 +804,20 @@ def moe_norm_out(f, x, post_weight=None, post_bias=None, gate=None, residual_sca
             gate_kind, gp = MOE_GATE_TOKEN, _dense(gate, dt, gshape, "gate")
         else:
             raise ValueError(f"gate: expected [{d}], [{T}], [{T}, 1] or [{T}, {d}], got {gshape}")
+    fp, fs = _rows(f, dt, shape, "f")
+    xp, xs = _rows(x, dt, shape, "x")
     if x_out is None:
         x_out = torch.empty(shape, dtype=dt, device=x.device)
+        xo, xos = x_out.data_ptr(), d
+    else:
+        xo, xos = _rows(x_out, dt, shape, "x_out")
     np_, ns = None, 0
     if next_norm:
         if next_out is None:
             next_out = torch.empty(shape, dtype=dt, device=x.device)
-        np_, ns = _rows(next_out, dt, shape, "next_out")
-    fp, fs = _rows(f, dt, shape, "f")
-    xp, xs = _rows(x, dt, shape, "x")
-    xo, xos = _rows(x_out, dt, shape, "x_out")
+            np_, ns = next_out.data_ptr(), d
+        else:
+            np_, ns = _rows(next_out, dt, shape, "next_out")
     vec = (d,)
     _check("moe_norm_out",
            _fn("moe_norm_out")(n, fp, fs, xp, xs, 1 if post_norm else 0,
@@ -846,7 +852,9 @@ def moe_kv_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cac
         qp, qs = _heads(q, dt, shape, "q")
         if q_out is None:
             q_out = torch.empty(shape, dtype=dt, device=q.device)
-        qo, qos = _heads(q_out, dt, shape, "q_out")
+            qo, qos = q_out.data_ptr(), shape[1] * D
+        else:
+            qo, qos = _heads(q_out, dt, shape, "q_out")
     shape = (T, hkv, D)
     kp, ks = _heads(k, dt, shape, "k")
     vp, vs = _heads(v, dt, shape, "v")
@@ -885,12 +893,14 @@ def moe_prefix_attention(kv: MoeKv, q, k_cache, v_cache, prefix_pages, prefix_le
     dt = _kv_dtype(kv)
     T, B, hq = q.shape[0], kv_lens.shape[0], kv.num_q_heads
     shape = (T, hq, kv.head_dim)
+    qp, qs = _heads(q, dt, shape, "q")
     if out is None:
         out = torch.empty(shape, dtype=dt, device=q.device)
+        op, os_ = out.data_ptr(), hq * shape[2]
+    else:
+        op, os_ = _heads(out, dt, shape, "out")
     if lse is None and want_lse:
         lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-    qp, qs = _heads(q, dt, shape, "q")
-    op, os_ = _heads(out, dt, shape, "out")
     cache = (kv.num_pages, kv.num_kv_heads, kv.page_size, kv.head_dim)
     max_pages, table = 0, None
     if page_table is not None:
