@@ -299,3 +299,41 @@ def test_pages_past_the_end_are_not_looked_at():
     c.table[0, 2:] = -1
     c.table[1, 1:] = 1 << 25
     c.check()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, FP16), (128, BF16)])
+@pytest.mark.parametrize("B,prefix,own", [(1, 130, 2000), (3, 128, 5000), (128, 1000, 40), (129, 40, 190),
+                                          (300, 257, 20), (700, 129, 33)])
+def test_prefix_tiles_beside_own_rows(B, prefix, own, D, dtype):
+    # few and many sequences, either part the longer one: 32 heads a key head, so
+    # that the prefix's rows are many and a sequence's few
+    qs = [1 + (b % 7 == 3) for b in range(B)]
+    lens = [max(q, own - (11 * b) % (own // 2 + 1)) for b, q in enumerate(qs)]
+    lens[B // 2] = 0
+    Case(qs, lens, prefix, hq=32, hkv=1, D=D, dtype=dtype, page=16).check()
+
+
+def test_calls_in_a_row_see_their_own_lengths():
+    # nothing waits on the host between the calls and the changes of their inputs
+    c = Case([1] * 40, [400] * 40, 300, hq=16, hkv=2, D=128, page=16)
+    ws = c.workspace()
+    sets = [torch.tensor([1 + (i * s + 13 * s) % 400 for i in range(40)], dtype=torch.int32, device="cuda")
+            for s in range(1, 9)]
+    want = []
+    for s in sets:
+        c.lens.copy_(s)
+        want.append(c.run(ws=ws)[0])
+        torch.cuda.synchronize()
+    q = c.q.clone()
+    got = []
+    for _ in range(3):
+        for s in sets:
+            c.lens.copy_(s)
+            c.q.copy_(q)
+            got.append(c.run(ws=ws)[0])
+            c.q.zero_()
+            c.lens.zero_()
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % len(sets)])
+    assert moe.moe_get_device_status(ws) == 0
