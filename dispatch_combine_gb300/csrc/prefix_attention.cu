@@ -62,20 +62,20 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
   constexpr int kBatch = W > 1 ? 8 : 4;  // with many rows the other warps hide a row's way
   const PrefixAttnArgs &a = g.a;
   const int t = blockIdx.x, lane = threadIdx.x & 31;
-  // the token's sequence: how many end at or before it
+  // the token's sequence: how many end at or before it, by a search 32 ways at a
+  // time (4096 sequences of up to 512 rows over 1024, 16 + 2 heads: 257 us a call,
+  // 285 when every CTA counts them all; up to 64 sequences: the same)
   int b = t;
   if (a.q_offsets) {
-    __shared__ int s_ends[8];
-    int n = 0;
-#pragma unroll 1
-    for (int i = threadIdx.x; i < a.B; i += blockDim.x) n += a.q_offsets[i + 1] <= t;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-    if (lane == 0) s_ends[threadIdx.x >> 5] = n;
-    __syncthreads();
     b = 0;
 #pragma unroll 1
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) b += s_ends[w];
+    for (int n = a.B; n > 0;) {  // the answer is in [b, b + n]
+      const int part = (n + 31) >> 5;
+      const int probe = b + min((lane + 1) * part, n);
+      const int k = __popc(__ballot_sync(0xffffffffu, a.q_offsets[probe] <= t));
+      b += min(k * part, n);
+      n = max(min(part, n - k * part) - 1, 0);
+    }
   }
   if (!alone) pdl_begin();
   const int h0 = (blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)) / W;
