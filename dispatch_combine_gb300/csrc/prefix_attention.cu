@@ -49,6 +49,14 @@ __device__ __forceinline__ int2 span_of(const AttnArgs &g, int64_t place, bool r
   return w;
 }
 
+// Whether token t of sequence b sees a key.
+__device__ __forceinline__ bool sees_any(const AttnArgs &g, int b, int t) {
+  if (g.a.prefix_len > 0) return true;
+  bool x = false, y = false;
+  const Seq s = read_seq<SliceSteps>(g, b, &x, &y);
+  return s.len - s.nq + (t - s.q0) + 1 > 0;
+}
+
 // W warps per token and query head, each with every W-th batch of its parts
 // (one token has as many parts as its rows have workers, and little else to
 // fill the GPU).
@@ -190,15 +198,21 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
       l += s_o[warp + w][E][lane];
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  // A sum of zero: no key is visible, or every score is -infinity (an infinite
+  // element in the query, or a product past fp32), where the quotient is 0 / 0.
+  // A query with a NaN has left one in l.
+  float inv = 1.0f / l, lse_out = (ref + log2f(l)) * 0.6931471805599453f;
+  if (l == 0.0f) {
+    const bool seen = sees_any(g, b, t);
+    inv = seen ? NAN : 0.0f;
+    lse_out = seen ? NAN : -INFINITY;
+  }
   uint32_t *dst =
       reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.o) + t * a.o_stride + h * D) +
       lane * (E / 2);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<DTYPE>(o[e] * inv, o[e + 1] * inv);
-  if (a.lse && lane == 0)
-    a.lse[static_cast<int64_t>(t) * a.hq + h] =
-        l > 0.0f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(t) * a.hq + h] = lse_out;
 }
 
 // ---------------------------------------------------------------------------

@@ -262,7 +262,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const int r = m * 16 + h * 8 + gr;
       if (r >= rows) continue;
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN stays one
       float *dst = g.part_o + (slot + r) * D + 2 * t;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
@@ -270,7 +270,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
             make_float2(o[m][n][2 * h] * inv, o[m][n][2 * h + 1] * inv);
       if (t == 0)
         g.part_lse[slot + r] =
-            sum > 0.0f ? mx[m][h] * sl2 - Prob<DTYPE>::kOff + log2f(sum) : -INFINITY;
+            sum == 0.0f ? -INFINITY : mx[m][h] * sl2 - Prob<DTYPE>::kOff + log2f(sum);
     }
 }
 

@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (warp_live) {
         const float2 lv = unpack_f32x2(l2);
         const float l = lv.x + lv.y;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a NaN stays one
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
         // in powers of two
-        if (mine) g.part_lse[at] = l > 0.0f ? m * sl2 - kOff + log2f(l) : -INFINITY;
+        if (mine) g.part_lse[at] = l == 0.0f ? -INFINITY : m * sl2 - kOff + log2f(l);
       }
     }
   }
