@@ -373,6 +373,12 @@ struct Prob {
   static constexpr float kLag = DTYPE == MOE_DTYPE_FP16 ? 5.0f : 8.0f;
 };
 constexpr float kLog2e = 1.4426950408889634f;
+// The lag in units of a score; finite for the smallest scales too, whose
+// reciprocal is not: -infinity + lag is the first maximum's bar.
+template <int DTYPE>
+__device__ __forceinline__ float score_lag(float sl2) {
+  return fminf(Prob<DTYPE>::kLag / sl2, 3.4028234663852886e38f);
+}
 
 constexpr int kTile = TileSteps::kKeys;    // keys per tile
 constexpr int kSlice = SliceSteps::kKeys;  // keys per slice

@@ -151,7 +151,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
     l[m][0] = l[m][1] = 0.0f;
   }
   const float sl2 = a.scale * kLog2e;
-  const float lag = Prob<DTYPE>::kLag / sl2;
+  const float lag = score_lag<DTYPE>(sl2);
   const int all_seen = min(x.kv_len, x.lim0);  // keys that every token sees
 #pragma unroll 1
   for (int s = x.s0 - (C::STAGES - 1); s < x.s1; ++s) {

@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t to = tmem_base + lane_base + C::T_O + w * D;
     constexpr float kOff = Prob<DTYPE>::kOff;
     const float sl2 = a.scale * kLog2e;
-    const float lag = Prob<DTYPE>::kLag / sl2;
+    const float lag = score_lag<DTYPE>(sl2);
     const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
     // segments, uses of s_full and o_full, V tiles and steps so far
     uint32_t nseg = 0, s_use = 0, o_use = 0, vc = 0, step = 0;

@@ -57,3 +57,12 @@ def test_a_query_that_is_not_finite_gives_nan(name, D, dtype, value):
     assert ((o.double() - ro).abs() <= bound)[~rows].all()
     assert ((lse.double() - rl).abs() <= 1e-4 + 2.0 ** -23 * rl.abs())[~rows].all()
     assert moe.moe_get_device_status(c.ws) == 0
+
+
+@pytest.mark.parametrize("name", ROUTES)
+@pytest.mark.parametrize("D,dtype", FORMS)
+@pytest.mark.parametrize("scale", [1e-44, 1e-38, 2e-36, 1e-20])
+def test_scales_near_the_smallest(name, D, dtype, scale):
+    # every score is as good as zero: the mean of the values, the log of their number
+    c = route(name, D, dtype)
+    c.check(got=c.run(scale=scale), scale=scale)
