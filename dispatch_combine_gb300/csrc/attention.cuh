@@ -363,15 +363,45 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The probabilities of both kernels are 2^(s * sl2 - m * sl2 + off): fp16 ones
-// are kept 2^10 up, away from its subnormals; the running maximum m may lag
-// by `lag` powers of two behind the true one before sums and accumulators are
-// rescaled, so they stay below 2^15 (fp16 holds 65504) or 2^8 (bf16).
+// The probabilities of both kernels are 2^(s * sl2 + c0), c0 = off - m * sl2:
+// fp16 ones are kept 2^10 up, away from its subnormals; the running maximum m
+// may lag by `lag` powers of two behind the true one before sums and
+// accumulators are rescaled, so they stay below 2^15 (fp16 holds 65504) or 2^8
+// (bf16).  c0 is one fp32 number, the same for all keys that it serves, so its
+// rounding cancels as long as the sums are rescaled by, and the log-sum-exp taken
+// from, this number.  It must not carry a probability past its type: up to
+// kMost it rounds by at most 1/2 (2^15.5) or 32 (2^40).  Past it a row's result
+// is NaN (taking the maximum off the scores first has no such end, but as one
+// more addition per score, or a branch around the exponentials for such rows
+// alone, 256 queries over 32768 rows took 231 to 255 us at head size 128
+// instead of 212).
 template <int DTYPE>
 struct Prob {
   static constexpr float kOff = DTYPE == MOE_DTYPE_FP16 ? 10.0f : 0.0f;
   static constexpr float kLag = DTYPE == MOE_DTYPE_FP16 ? 5.0f : 8.0f;
+  static constexpr float kMost = DTYPE == MOE_DTYPE_FP16 ? 16777216.0f : 1073741824.0f;
 };
+template <int DTYPE>
+__device__ __forceinline__ float prob_offset(float m, float sl2) {
+  return m == -INFINITY ? Prob<DTYPE>::kOff : fmaf(-m, sl2, Prob<DTYPE>::kOff);
+}
+// What sums taken with maximum m become with m1 > m.
+template <int DTYPE>
+__device__ __forceinline__ float rescale(float m, float m1, float sl2) {
+  return m == -INFINITY ? 0.0f : ex2(prob_offset<DTYPE>(m1, sl2) - prob_offset<DTYPE>(m, sl2));
+}
+// A part's scale and log2-sum-exp from its sum l: 0 and -infinity where it saw
+// nothing; a NaN (a query that is not finite, scores past the range) stays one.
+struct PartEnd {
+  float inv, lse;
+};
+template <int DTYPE>
+__device__ __forceinline__ PartEnd end_part(float m, float l, float sl2) {
+  const float c0 = prob_offset<DTYPE>(m, sl2);
+  if (l == 0.0f) return {0.0f, -INFINITY};
+  if (fabsf(c0) > Prob<DTYPE>::kMost) l = NAN;
+  return {1.0f / l, log2f(l) - c0};
+}
 constexpr float kLog2e = 1.4426950408889634f;
 // The lag in units of a score; finite for the smallest scales too, whose
 // reciprocal is not: -infinity + lag is the first maximum's bar.

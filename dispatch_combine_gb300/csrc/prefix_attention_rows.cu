@@ -197,7 +197,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         moves |= fmaxf(fmaxf(sc[m][0][2 * h], sc[m][0][2 * h + 1]),
-                       fmaxf(sc[m][1][2 * h], sc[m][1][2 * h + 1])) > mx[m][h] + lag;
+                       fmaxf(sc[m][1][2 * h], sc[m][1][2 * h + 1])) - mx[m][h] > lag;
     if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -208,7 +208,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           if (top > mx[m][h]) {
-            const float f = ex2((mx[m][h] - top) * sl2);  // 0 at the first
+            const float f = rescale<DTYPE>(mx[m][h], top, sl2);
             mx[m][h] = top;
             l[m][h] *= f;
 #pragma unroll
@@ -225,8 +225,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float c0 = mx[m][h] == -INFINITY ? Prob<DTYPE>::kOff
-                                               : Prob<DTYPE>::kOff - mx[m][h] * sl2;
+        const float c0 = prob_offset<DTYPE>(mx[m][h], sl2);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const float e0 = ex2(fmaf(sc[m][n][2 * h], sl2, c0));
@@ -262,15 +261,13 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const int r = m * 16 + h * 8 + gr;
       if (r >= rows) continue;
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN stays one
+      const PartEnd end = end_part<DTYPE>(mx[m][h], sum, sl2);
       float *dst = g.part_o + (slot + r) * D + 2 * t;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
         *reinterpret_cast<float2 *>(dst + 8 * n) =
-            make_float2(o[m][n][2 * h] * inv, o[m][n][2 * h + 1] * inv);
-      if (t == 0)
-        g.part_lse[slot + r] =
-            sum == 0.0f ? -INFINITY : mx[m][h] * sl2 - Prob<DTYPE>::kOff + log2f(sum);
+            make_float2(o[m][n][2 * h] * end.inv, o[m][n][2 * h + 1] * end.inv);
+      if (t == 0) g.part_lse[slot + r] = end.lse;  // in powers of two
     }
 }
 

@@ -583,7 +583,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t ts = tmem_base + lane_base + w * 128;
     const uint32_t tp = tmem_base + lane_base + C::T_P + w * C::T_P_STEP;
     const uint32_t to = tmem_base + lane_base + C::T_O + w * D;
-    constexpr float kOff = Prob<DTYPE>::kOff;
     const float sl2 = a.scale * kLog2e;
     const float lag = score_lag<DTYPE>(sl2);
     const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
@@ -680,14 +679,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             asm("max.f32 %0, %0, %1, %2;" : "+f"(tops[c]) : "f"(x), "f"(y));
           }
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        const bool moves = top > m + lag;
+        const bool moves = top - m > lag;
         bool waited = false;
         if (rare(__any_sync(0xffffffffu, moves))) {
           if (!last_product()) break;
           waited = true;
           const float m1 = moves ? top : m;
-          // 0 where the row has seen nothing yet
-          const float f = moves ? ex2((m - m1) * sl2) : 1.0f;
+          const float f = moves ? rescale<DTYPE>(m, m1, sl2) : 1.0f;
           m = m1;
           const float2 lv = unpack_f32x2(l2);
           l2 = pack_f32x2(lv.x * f, lv.y * f);
@@ -704,7 +702,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
         }
-        const float c0 = m == -INFINITY ? kOff : kOff - m * sl2;
+        const float c0 = prob_offset<DTYPE>(m, sl2);
         const uint64_t c0x2 = pack_f32x2(c0, c0);
         uint64_t sums[4] = {l2, 0, 0, 0};
 #pragma unroll
@@ -748,8 +746,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc_fence_after();
       if (warp_live) {
         const float2 lv = unpack_f32x2(l2);
-        const float l = lv.x + lv.y;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a NaN stays one
+        const PartEnd end = end_part<DTYPE>(m, lv.x + lv.y, sl2);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -762,13 +759,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               uint32_t x[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                x[e] = __float_as_uint(__uint_as_float(o[8 * j + e]) * inv);
+                x[e] = __float_as_uint(__uint_as_float(o[8 * j + e]) * end.inv);
               st_global_v8(g.part_o + at * D + c * 32 + j * 8, x);
             }
           }
         }
-        // in powers of two
-        if (mine) g.part_lse[at] = l == 0.0f ? -INFINITY : m * sl2 - kOff + log2f(l);
+        if (mine) g.part_lse[at] = end.lse;  // in powers of two
       }
     }
   }

@@ -589,7 +589,8 @@ moe_status_t moe_kv_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t
  *   o [T, num_q_heads, head_dim] with token stride o_stride; lse [T,
  *   num_q_heads] fp32 (NULL to skip): ln of the row's sum of exponentials.
  *   A token that sees nothing gets zeros and -inf; a head whose query holds a
- *   NaN or an infinity, or has scores past fp32's range, gets NaN in both.
+ *   NaN or an infinity, or whose largest score passes 1.1e7 (fp16) or 7e8 (bf16)
+ *   in magnitude, gets NaN in both.
  *   scores are scale * q.k (scale > 0, finite); softmax statistics and sums are fp32, the
  *   probabilities are rounded to the cache's type for the product with V.
  * What lies in pages past kv_lens or past the prefix's end is never used,
