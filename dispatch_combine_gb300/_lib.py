@@ -743,6 +743,28 @@ def _dense(t, dtype, shape, name):
     _expect(t, dtype, shape, name)
 
 
+def _on(stream, make):
+    """make() with what it allocates and launches on the call's stream, which
+    the kernel of the call will use it on."""
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _empty(shape, dtype, device, stream):
+    """An output: its memory is the call's stream's (memory from the current
+    stream's pool may still be in use there), and is not given away while the
+    current stream, which it is returned to, has work on it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    out = _on(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
+    out.record_stream(torch.cuda.current_stream())
+    return out
+
+
 @functools.lru_cache(maxsize=256)
 def _norm_struct(T, d, kind, dtype, eps, weight_offset):
     return ctypes.byref(MoeNorm(T, d, int(kind), dtype, float(eps), float(weight_offset)))
@@ -762,7 +784,7 @@ def moe_norm_in(x, weight=None, bias=None, kind=MOE_NORM_RMS, eps=1e-6, weight_o
     n = _norm_struct(T, d, kind, _dtype(dt), eps, weight_offset)
     xp, xs = _rows(x, dt, shape, "x")
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=x.device)
+        out = _empty(shape, dt, x.device, stream)
         op, os_ = out.data_ptr(), d
     else:
         op, os_ = _rows(out, dt, shape, "out")
@@ -800,21 +822,21 @@ def moe_norm_out(f, x, post_weight=None, post_bias=None, gate=None, residual_sca
         elif gshape == (d,):
             gate_kind, gp = MOE_GATE_CHANNEL, _dense(gate, dt, gshape, "gate")
         elif gshape in ((T,), (T, 1)):
-            gate = gate.contiguous()  # a copy is kept until the launch
+            gate = _on(stream, gate.contiguous)  # a copy is kept until the launch
             gate_kind, gp = MOE_GATE_TOKEN, _dense(gate, dt, gshape, "gate")
         else:
             raise ValueError(f"gate: expected [{d}], [{T}], [{T}, 1] or [{T}, {d}], got {gshape}")
     fp, fs = _rows(f, dt, shape, "f")
     xp, xs = _rows(x, dt, shape, "x")
     if x_out is None:
-        x_out = torch.empty(shape, dtype=dt, device=x.device)
+        x_out = _empty(shape, dt, x.device, stream)
         xo, xos = x_out.data_ptr(), d
     else:
         xo, xos = _rows(x_out, dt, shape, "x_out")
     np_, ns = None, 0
     if next_norm:
         if next_out is None:
-            next_out = torch.empty(shape, dtype=dt, device=x.device)
+            next_out = _empty(shape, dt, x.device, stream)
             np_, ns = next_out.data_ptr(), d
         else:
             np_, ns = _rows(next_out, dt, shape, "next_out")
@@ -851,7 +873,7 @@ def moe_kv_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cac
         shape = (T, kv.num_q_heads, D)
         qp, qs = _heads(q, dt, shape, "q")
         if q_out is None:
-            q_out = torch.empty(shape, dtype=dt, device=q.device)
+            q_out = _empty(shape, dt, q.device, stream)
             qo, qos = q_out.data_ptr(), shape[1] * D
         else:
             qo, qos = _heads(q_out, dt, shape, "q_out")
@@ -895,12 +917,12 @@ def moe_prefix_attention(kv: MoeKv, q, k_cache, v_cache, prefix_pages, prefix_le
     shape = (T, hq, kv.head_dim)
     qp, qs = _heads(q, dt, shape, "q")
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=q.device)
+        out = _empty(shape, dt, q.device, stream)
         op, os_ = out.data_ptr(), hq * shape[2]
     else:
         op, os_ = _heads(out, dt, shape, "out")
     if lse is None and want_lse:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+        lse = _empty((T, hq), torch.float32, q.device, stream)
     cache = (kv.num_pages, kv.num_kv_heads, kv.page_size, kv.head_dim)
     max_pages, table = 0, None
     if page_table is not None:
