@@ -225,12 +225,29 @@ constexpr int kPrefixRows = 32, kOwnRows = 64;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+// Units of one kind, and rows of partial results for them.
+struct Slots {
+  int64_t units, rows;
+};
 struct Scratch {
   size_t span, lse, o, bytes;
 };
+Scratch layout(int B, const Slots &prefix, const Slots &own, int D) {
+  const size_t units = static_cast<size_t>(prefix.units + own.units);
+  const size_t rows = static_cast<size_t>(prefix.rows + own.rows);
+  Scratch s;
+  s.span = up256(sizeof(SeqMeta) * static_cast<size_t>(B));
+  s.lse = up256(s.span + sizeof(int2) * units);
+  s.o = up256(s.lse + 4 * rows);
+  s.bytes = up256(s.o + 4 * rows * D);
+  return s;
+}
+struct Need {
+  Slots prefix, own;
+};
 
 // own_rows: whether sequences can have rows of their own
-Scratch plan(AttnArgs &g, int T, int B, int max_q, int hq, int hkv, int D, int prefix_len,
+Need plan(AttnArgs &g, int T, int B, int max_q, int hq, int hkv, int D, int prefix_len,
              bool own_rows, int ctas) {
   const int G = hq / hkv, nq = std::max(1, std::min(max_q, T));
   g.G = G;
@@ -286,28 +303,25 @@ Scratch plan(AttnArgs &g, int T, int B, int max_q, int hq, int hkv, int D, int p
     g.own.tok = g.s_wide ? 2 * g.tpt : g.tpt;
     g.own.rows = g.s_box * G;
   }
-  int64_t rows = 0, units = 0;
+  Need n = {};
   if (g.r_prefix) {
-    units = static_cast<int64_t>(hkv) * g.r_blocks;
-    rows = (static_cast<int64_t>(hkv) * g.r_blocks + kMaxCtas * kRowWarps) * g.r_rows;
+    n.prefix.units = static_cast<int64_t>(hkv) * g.r_blocks;
+    n.prefix.rows = (n.prefix.units + kMaxCtas * kRowWarps) * g.r_rows;
   } else if (g.p_on) {  // (hkv * groups + gangs) * gang slots, whatever the grid
-    units = static_cast<int64_t>(hkv) * (g.p_blocks + 16);
-    rows = (units + kMaxCtas) * 2 * g.p_rows;
+    n.prefix.units = static_cast<int64_t>(hkv) * (g.p_blocks + 16);
+    n.prefix.rows = (n.prefix.units + kMaxCtas) * 2 * g.p_rows;
   }
-  g.own.slot0 = rows;
-  g.own.span0 = static_cast<int>(units);
+  g.own.slot0 = n.prefix.rows;
+  g.own.span0 = static_cast<int>(n.prefix.units);
   if (own) {
-    const int64_t more = static_cast<int64_t>(hkv) * (B + T / g.own.tok);
-    units += more;
-    rows += g.own_rows_kernel ? (more + kMaxCtas * kRowWarps) * g.own.rows
-                              : (more + kMaxCtas) * 2 * g.own.rows;
+    // blocks of all sequences: the tokens may lie in any of them, max_q in each
+    const int64_t blocks = std::min<int64_t>(
+        B + T / g.own.tok, static_cast<int64_t>(B) * ((nq + g.own.tok - 1) / g.own.tok));
+    n.own.units = blocks * hkv;
+    n.own.rows = g.own_rows_kernel ? (n.own.units + kMaxCtas * kRowWarps) * g.own.rows
+                                   : (n.own.units + kMaxCtas) * 2 * g.own.rows;
   }
-  Scratch s;
-  s.span = up256(sizeof(SeqMeta) * static_cast<size_t>(B));
-  s.lse = up256(s.span + sizeof(int2) * static_cast<size_t>(units));
-  s.o = up256(s.lse + 4 * static_cast<size_t>(rows));
-  s.bytes = up256(s.o + 4 * static_cast<size_t>(rows) * D);
-  return s;
+  return n;
 }
 
 template <int DTYPE, int D>
@@ -333,8 +347,23 @@ cudaError_t join(const AttnArgs &g, int ctas, cudaStream_t s) {
 
 size_t prefix_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D,
                                       int prefix_len) {
+  // What no smaller call passes.  Either kernel's need grows with every argument
+  // (a unit of the rows kernel holds as many tokens as fit 32 rows, and all of up
+  // to 32 rows are one unit), but the rows kernel has eight workers per CTA where
+  // the tiles kernel has one, so its largest call can need more than the tiles
+  // kernel's smallest: the larger of the two counts.
   AttnArgs g = {};
-  return plan(g, T, B, max_q, hq, hkv, D, prefix_len, true, kMaxCtas).bytes;
+  Need n = plan(g, T, B, max_q, hq, hkv, D, prefix_len, true, kMaxCtas);
+  const int G = hq / hkv;
+  if (G <= kPrefixRows) {
+    const Slots p = plan(g = {}, std::min(T, kPrefixRows / G), B, max_q, hq, hkv, D, prefix_len, true,
+                         kMaxCtas).prefix;
+    const Slots o = plan(g = {}, T, B, std::min(max_q, kOwnRows / G), hq, hkv, D, prefix_len, true,
+                         kMaxCtas).own;
+    n.prefix = {std::max(n.prefix.units, p.units), std::max(n.prefix.rows, p.rows)};
+    n.own = {std::max(n.own.units, o.units), std::max(n.own.rows, o.rows)};
+  }
+  return layout(B, n.prefix, n.own, D).bytes;
 }
 
 cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, int dtype, cudaStream_t s) {
@@ -343,8 +372,8 @@ cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, int dtype, cudaStre
   g.a = a;
   if (!g.a.wait_limit_ns) g.a.wait_limit_ns = kDefaultWaitLimitNs;
   const int ctas = std::min(num_sms(), kMaxCtas);
-  const Scratch sc =
-      plan(g, a.T, a.B, a.max_q, a.hq, a.hkv, a.D, a.prefix_len, a.max_pages > 0, ctas);
+  const Need n = plan(g, a.T, a.B, a.max_q, a.hq, a.hkv, a.D, a.prefix_len, a.max_pages > 0, ctas);
+  const Scratch sc = layout(a.B, n.prefix, n.own, a.D);
   g.meta = reinterpret_cast<SeqMeta *>(a.scratch);
   g.span = reinterpret_cast<int2 *>(a.scratch + sc.span);
   g.part_lse = reinterpret_cast<float *>(a.scratch + sc.lse);

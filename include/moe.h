@@ -601,6 +601,8 @@ moe_status_t moe_kv_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t
  * are clamped, the affected rows undefined and nothing outside the buffers is
  * touched.
  * num_seqs <= 4096 (MOE_ERR_UNSUPPORTED beyond).
+ * A workspace sized for some T, num_seqs, max_q and prefix_len (and heads)
+ * serves every call in which none of the four is larger.
  */
 moe_status_t moe_prefix_attention_workspace_size(const moe_kv_t *kv, int32_t T, int32_t num_seqs,
                                                  int32_t max_q, int32_t prefix_len,
