@@ -49,12 +49,18 @@ __device__ __forceinline__ int2 span_of(const AttnArgs &g, int64_t place, bool r
   return w;
 }
 
-// Whether token t of sequence b sees a key.
-__device__ __forceinline__ bool sees_any(const AttnArgs &g, int b, int t) {
-  if (g.a.prefix_len > 0) return true;
-  bool x = false, y = false;
-  const Seq s = read_seq<SliceSteps>(g, b, &x, &y);
-  return s.len - s.nq + (t - s.q0) + 1 > 0;
+// A whole CTA, where there are no pages of own rows: what the scan of the lengths
+// would have found wrong with them and the offsets.
+__device__ __forceinline__ void report_bad(const PrefixAttnArgs &a) {
+  bool bad = false;
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    bad |= a.kv_lens[b] != 0;
+    if (a.q_offsets) {
+      const int64_t q0 = a.q_offsets[b], q1 = a.q_offsets[b + 1];
+      bad |= q0 < 0 || q1 < q0 || q1 > a.T || q1 - q0 > a.max_q;
+    }
+  }
+  if (bad) set_status(a.status, kStatusBadId);
 }
 
 // W warps per token and query head, each with every W-th batch of its parts
@@ -66,6 +72,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
   // the call, so the call's inputs can be read ahead of this one's own wait.
   const bool alone = !g.r_on && !g.t_on;
   if (alone) pdl_begin();
+  if (!g.own_rows_kernel && !g.own_on && blockIdx.x == 0 && blockIdx.y == 0) report_bad(g.a);
   constexpr int E = D / 32;
   constexpr int kBatch = W > 1 ? 8 : 4;  // with many rows the other warps hide a row's way
   const PrefixAttnArgs &a = g.a;
@@ -201,18 +208,24 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
   // A sum of zero: no key is visible, or every score is -infinity (an infinite
   // element in the query, or a product past fp32), where the quotient is 0 / 0.
   // A query with a NaN has left one in l.
-  float inv = 1.0f / l, lse_out = (ref + log2f(l)) * 0.6931471805599453f;
+  float inv = 1.0f / l;
   if (l == 0.0f) {
-    const bool seen = sees_any(g, b, t);
-    inv = seen ? NAN : 0.0f;
-    lse_out = seen ? NAN : -INFINITY;
+    bool seen = a.prefix_len > 0;
+    if (m.steps > 0) {
+      const int nq = a.q_offsets ? a.q_offsets[b + 1] - q0 : 1;
+      seen |= a.kv_lens[b] - nq + (t - q0) + 1 > 0;
+    }
+    if (seen) l = NAN;
+    inv = l;
   }
   uint32_t *dst =
       reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.o) + t * a.o_stride + h * D) +
       lane * (E / 2);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<DTYPE>(o[e] * inv, o[e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(t) * a.hq + h] = lse_out;
+  if (a.lse && lane == 0)
+    a.lse[static_cast<int64_t>(t) * a.hq + h] =
+        l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------------------
