@@ -72,10 +72,14 @@ moe_status_t check_ws(const void *ws, size_t ws_bytes, size_t need) {
   return MOE_OK;
 }
 
+// Key numbers are int, and reach past a length by a tile and a block of tokens.
+constexpr int64_t kMostKeys = (int64_t{1} << 31) - 1024;
+
 moe_status_t check_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, int32_t max_q,
                              int32_t prefix_len) {
   MOE_TRY(check_kv(kv));
-  if (T < 0 || num_seqs < 0 || max_q < 1 || prefix_len < 0) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || num_seqs < 0 || max_q < 1 || prefix_len < 0 || prefix_len > kMostKeys)
+    return MOE_ERR_INVALID_ARG;
   if (num_seqs > 4096) return MOE_ERR_UNSUPPORTED;
   // the partial results are indexed with 32-bit row numbers
   if (static_cast<int64_t>(T) * kv->num_q_heads >= (int64_t{1} << 30)) return MOE_ERR_UNSUPPORTED;
@@ -221,7 +225,7 @@ moe_status_t moe_prefix_attention(const moe_kv_t *kv, int32_t T, int32_t num_seq
   MOE_TRY(check_attention(kv, T, num_seqs, max_q, prefix_len));
   if (max_pages < 0 || !(scale > 0.0f) || !std::isfinite(scale))
     return MOE_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(max_pages) * kv->page_size >= (int64_t{1} << 31))
+  if (static_cast<int64_t>(max_pages) * kv->page_size > kMostKeys)
     return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!q_offsets && T != num_seqs) return MOE_ERR_INVALID_ARG;

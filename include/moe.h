@@ -600,7 +600,8 @@ moe_status_t moe_kv_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t
  * give a sequence more than max_q tokens set MOE_ERR_INVALID_ARG; the values
  * are clamped, the affected rows undefined and nothing outside the buffers is
  * touched.
- * num_seqs <= 4096 (MOE_ERR_UNSUPPORTED beyond).
+ * num_seqs <= 4096 (MOE_ERR_UNSUPPORTED beyond); prefix_len and max_pages *
+ * page_size <= 2^31 - 1024 (MOE_ERR_INVALID_ARG beyond).
  * A workspace sized for some T, num_seqs, max_q and prefix_len (and heads)
  * serves every call in which none of the four is larger.
  */
