@@ -196,7 +196,7 @@ template <int DTYPE, bool TWO>
 cudaError_t run(const NormArgs &a, cudaStream_t s) {
   const int nvec = a.d / 8;
   if (nvec <= 64) {  // a row per warp, 8 rows per CTA
-    const unsigned ctas = static_cast<unsigned>((a.T + 7) / 8);
+    const unsigned ctas = (static_cast<unsigned>(a.T) + 7u) / 8u;
     if (nvec <= 32)
       MOE_LAUNCH_PDL(norm_kernel<DTYPE, 1, true, TWO>, ctas, 256, 0, s, a);
     else
