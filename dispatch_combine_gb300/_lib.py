@@ -765,9 +765,9 @@ def _empty(shape, dtype, device, stream):
     return out
 
 
-@functools.lru_cache(maxsize=256)
+@functools.lru_cache(maxsize=256)  # by plain numbers: an object's value can change
 def _norm_struct(T, d, kind, dtype, eps, weight_offset):
-    return ctypes.byref(MoeNorm(T, d, int(kind), dtype, float(eps), float(weight_offset)))
+    return ctypes.byref(MoeNorm(T, d, kind, dtype, eps, weight_offset))
 
 
 def _fn(name):
@@ -781,7 +781,7 @@ def moe_norm_in(x, weight=None, bias=None, kind=MOE_NORM_RMS, eps=1e-6, weight_o
         raise ValueError("x: expected [T, d]")
     shape, dt = x.shape, x.dtype
     T, d = shape
-    n = _norm_struct(T, d, kind, _dtype(dt), eps, weight_offset)
+    n = _norm_struct(T, d, int(kind), _dtype(dt), float(eps), float(weight_offset))
     xp, xs = _rows(x, dt, shape, "x")
     if out is None:
         out = _empty(shape, dt, x.device, stream)
@@ -808,7 +808,7 @@ def moe_norm_out(f, x, post_weight=None, post_bias=None, gate=None, residual_sca
         raise ValueError("x: expected [T, d]")
     shape, dt = x.shape, x.dtype
     T, d = shape
-    n = _norm_struct(T, d, kind, _dtype(dt), eps, weight_offset)
+    n = _norm_struct(T, d, int(kind), _dtype(dt), float(eps), float(weight_offset))
     if post_norm is None:
         post_norm = post_weight is not None
     if next_norm is None:
