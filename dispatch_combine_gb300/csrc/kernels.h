@@ -255,7 +255,6 @@ struct PrefixAttnArgs {
   int T, B, max_q, hq, hkv, D, page_shift, num_pages, prefix_len, max_pages;
   float scale;
   uint8_t *scratch;  // prefix_attention_scratch_bytes
-  uint64_t wait_limit_ns;  // 0: kDefaultWaitLimitNs
 };
 size_t prefix_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D,
                                       int prefix_len);

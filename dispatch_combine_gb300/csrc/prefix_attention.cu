@@ -383,7 +383,6 @@ cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, int dtype, cudaStre
   if (a.T == 0) return cudaSuccess;
   AttnArgs g = {};
   g.a = a;
-  if (!g.a.wait_limit_ns) g.a.wait_limit_ns = kDefaultWaitLimitNs;
   const int ctas = std::min(num_sms(), kMaxCtas);
   const Need n = plan(g, a.T, a.B, a.max_q, a.hq, a.hkv, a.D, a.prefix_len, a.max_pages > 0, ctas);
   const Scratch sc = layout(a.B, n.prefix, n.own, a.D);

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   B &bar = *reinterpret_cast<B *>(smem + C::BAR_OFF);
   volatile int *abort_flag = &bar.abort;
   const PrefixAttnArgs &a = g.a;
-  const uint64_t limit = a.wait_limit_ns;
+  constexpr uint64_t limit = kDefaultWaitLimitNs;
   __shared__ ScanShared<kAttnThreads> scan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bars = smem_u32(&bar);
