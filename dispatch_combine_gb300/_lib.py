@@ -776,7 +776,8 @@ def _fn(name):
 
 def moe_norm_in(x, weight=None, bias=None, kind=MOE_NORM_RMS, eps=1e-6, weight_offset=0.0,
                 out=None, stream=None):
-    """out = N(x) * (weight + weight_offset) + bias over the rows of x [T,d]."""
+    """out = N(x) * (weight + weight_offset) + bias over the rows of x [T,d];
+    without a weight the factor is 1."""
     if x.dim() != 2:
         raise ValueError("x: expected [T, d]")
     shape, dt = x.shape, x.dtype

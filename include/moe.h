@@ -490,15 +490,16 @@ typedef struct {
   int32_t kind;  /* moe_norm_kind_t */
   int32_t dtype; /* moe_dtype_t, of every tensor of the call */
   float eps;
-  float weight_offset; /* added to the norm weights: 0, or 1 for weights stored around zero */
+  float weight_offset; /* added to the norm weights: 0, or 1 for weights stored around zero;
+                          a weight that is NULL is a factor of 1 whatever this is */
 } moe_norm_t;
 
 /*
  * The norm in front of a block: out = N(x) * (weight + weight_offset) + bias,
  * N the statistic of `kind` over each row.
- *   x, out [T,d] with row strides x_stride / out_stride; weight [d] (NULL: 1),
- *   bias [d] (NULL: 0).  Statistics and arithmetic in fp32, one rounding at
- *   the end.  out may be x (same stride).
+ *   x, out [T,d] with row strides x_stride / out_stride; weight [d] (NULL: a
+ *   factor of 1), bias [d] (NULL: 0).  Statistics and arithmetic in fp32, one
+ *   rounding at the end.  out may be x (same stride).
  */
 moe_status_t moe_norm_in(const moe_norm_t *norm, const void *x, int64_t x_stride,
                          const void *weight, const void *bias, void *out, int64_t out_stride,
@@ -511,11 +512,11 @@ moe_status_t moe_norm_in(const moe_norm_t *norm, const void *x, int64_t x_stride
  *   r     = residual_scale * x + gate * v
  *   x_out = r rounded once
  *   next_out = N(r) * (next_weight + weight_offset) + next_bias
- *   post_norm != 0 selects the post norm (post_weight NULL: 1, post_bias
- *   NULL: 0); gate [d], [T] or [T,d] by gate_kind (a moe_gate_t; gate_stride
- *   is the row stride of the [T,d] form); next_out NULL skips the second
- *   norm (next_weight NULL: 1, next_bias NULL: 0).  The second norm is taken
- *   of r as it stands in fp32, not of the rounded x_out.
+ *   post_norm != 0 selects the post norm (post_weight NULL: a factor of 1,
+ *   post_bias NULL: 0); gate [d], [T] or [T,d] by gate_kind (a moe_gate_t;
+ *   gate_stride is the row stride of the [T,d] form); next_out NULL skips the
+ *   second norm (next_weight NULL: a factor of 1, next_bias NULL: 0).  The
+ *   second norm is taken of r as it stands in fp32, not of the rounded x_out.
  *   x_out may be x, and next_out may be f (same strides).
  */
 moe_status_t moe_norm_out(const moe_norm_t *norm, const void *f, int64_t f_stride, const void *x,
