@@ -7,7 +7,8 @@
 
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool aligned16(const void *p) { return aligned(p, 16); }
 
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
@@ -131,6 +132,7 @@ moe_status_t moe_norm_out(const moe_norm_t *norm, const void *f, int64_t f_strid
   if ((gate_kind == MOE_GATE_NONE) != (gate == nullptr)) return MOE_ERR_INVALID_ARG;
   if (gate_kind == MOE_GATE_FULL && !good_rows(gate, gate_stride, d)) return MOE_ERR_INVALID_ARG;
   if (gate_kind == MOE_GATE_CHANNEL && !aligned16(gate)) return MOE_ERR_INVALID_ARG;
+  if (gate_kind == MOE_GATE_TOKEN && !aligned(gate, 2)) return MOE_ERR_INVALID_ARG;
   // in place only row for row
   if ((x_out == x && x_out_stride != x_stride) || x_out == f || x_out == next_out ||
       (next_out == f && next_out_stride != f_stride) || next_out == x)
@@ -176,7 +178,9 @@ moe_status_t moe_kv_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t
   if (q && (!good_rows(q, q_stride, wq) || !good_rows(q_out, q_out_stride, wq) ||
             (q == q_out && q_stride != q_out_stride)))
     return MOE_ERR_INVALID_ARG;
-  if (rot_dim > 0 && (!positions || !inv_freq)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(slots, 4)) return MOE_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 4)))
+    return MOE_ERR_INVALID_ARG;
   if (ws) MOE_TRY(check_ws(ws, ws_bytes, kStatusBytes));
   moe::KvAppendArgs a = {};
   a.q = q;
@@ -234,6 +238,9 @@ moe_status_t moe_prefix_attention(const moe_kv_t *kv, int32_t T, int32_t num_seq
     return MOE_ERR_INVALID_ARG;
   if (num_seqs > 0 && (!kv_lens || (max_pages > 0 && !page_table))) return MOE_ERR_INVALID_ARG;
   if (prefix_len > 0 && !prefix_pages) return MOE_ERR_INVALID_ARG;
+  if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(lse, 4) ||
+      (max_pages > 0 && !aligned(page_table, 4)) || (prefix_len > 0 && !aligned(prefix_pages, 4)))
+    return MOE_ERR_INVALID_ARG;
   if ((prefix_len > 0 || max_pages > 0) &&
       (kv->num_pages == 0 || !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)))
     return MOE_ERR_INVALID_ARG;

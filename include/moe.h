@@ -462,6 +462,9 @@ moe_status_t moe_eplb_plan(const double *load, int32_t num_experts, int32_t num_
  * The rest of the decoder block around the layer: norms before and after a
  * block, the append to a paged key/value cache, and the attention that reads
  * it for a batch that shares a long prefix.  Forward only, like the layer.
+ * Row tensors, weights and caches are 16-byte aligned; positions, slots,
+ * lengths, offsets, page numbers, inv_freq, lse and a token's gate need the
+ * alignment of their elements only (MOE_ERR_INVALID_ARG otherwise).
  * ------------------------------------------------------------------------ */
 
 /* Element type of activations, weights and caches of these calls. */
@@ -564,7 +567,7 @@ typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_PAIRS = 1 } moe_rope_t;
  * MOE_ERR_INVALID_ARG in the workspace's status word (ws of at least 256
  * bytes; NULL: not reported).  Slots must be distinct: of two tokens with one
  * slot, either may win.
- * Pointers 16-byte aligned, strides multiples of 8.
+ * Strides are multiples of 8.
  */
 moe_status_t moe_kv_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t q_stride,
                            const void *k, int64_t k_stride, const void *v, int64_t v_stride,
