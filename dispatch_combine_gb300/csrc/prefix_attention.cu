@@ -232,9 +232,23 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g) {
 // the plan: everything the host knows, and the scratch it needs
 // ---------------------------------------------------------------------------
 
-// Rows up to which the rows kernel does the work: of the prefix (more rows
-// re-read it from L2), of one sequence's own.
-constexpr int kPrefixRows = 32, kOwnRows = 64;
+// Rows (tokens x query heads of a key head) that the rows kernel takes, as one
+// unit: of one sequence's own, or of the whole batch over the prefix.  Both
+// kernels on the same work (us, rows kernel and tiles kernel):
+//   own, 64 sequences x 4096, 8 key heads of 128: 16 rows 172 and 181, 20 rows
+// 205 and 183, 32 rows 214 and 188 (two 16-row blocks of accumulators of 128 do
+// not fit a warp's registers); key heads of 64, lengths up to 4096: 32 rows 62
+// and 72, 48 rows (two units, so keys and values read twice) 77 and 74;
+//   prefix of 1000, heads of 128: 16 rows 7.9 and 10.3, 20 rows 11.7 and 10.3;
+// heads of 64, 28 rows, beside own rows of up to 300 (which the rows kernel then
+// takes along): prefix 1000 12.1 and 15.2, 4000 16.2 and 20.8; without own rows:
+// 1000 8.1 and 9.1, 4000 12.7 and 11.5, 8192 20.8 and 12.2.
+constexpr int most_rows(int D) { return D == 64 ? 32 : 16; }
+constexpr int kRows = 16, kPrefixOf32 = 4096;  // any prefix; up to which 32 rows are taken
+bool own_by_rows(int D, int64_t rows) { return rows <= most_rows(D); }
+bool prefix_by_rows(int D, int64_t rows, int prefix_len) {
+  return rows <= (prefix_len <= kPrefixOf32 ? most_rows(D) : kRows);
+}
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -266,10 +280,10 @@ Need plan(AttnArgs &g, int T, int B, int max_q, int hq, int hkv, int D, int pref
   g.G = G;
   g.tpt = kTile / G;
   const bool own = own_rows && B > 0;
-  const bool small_prefix = static_cast<int64_t>(T) * G <= kPrefixRows;
+  const bool small_prefix = prefix_by_rows(D, static_cast<int64_t>(T) * G, prefix_len);
   g.r_prefix = prefix_len > 0 && small_prefix;
   g.p_on = prefix_len > 0 && !small_prefix;
-  g.own_rows_kernel = own && G <= kPrefixRows && static_cast<int64_t>(nq) * G <= kOwnRows;
+  g.own_rows_kernel = own && own_by_rows(D, static_cast<int64_t>(nq) * G);
   g.own_on = own && !g.own_rows_kernel;
   g.r_on = g.r_prefix || g.own_rows_kernel;
   g.t_on = g.p_on || g.own_on;
@@ -360,18 +374,17 @@ cudaError_t join(const AttnArgs &g, int ctas, cudaStream_t s) {
 
 size_t prefix_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D,
                                       int prefix_len) {
-  // What no smaller call passes.  Either kernel's need grows with every argument
-  // (a unit of the rows kernel holds as many tokens as fit 32 rows, and all of up
-  // to 32 rows are one unit), but the rows kernel has eight workers per CTA where
-  // the tiles kernel has one, so its largest call can need more than the tiles
-  // kernel's smallest: the larger of the two counts.
+  // What no smaller call passes.  Either kernel's need grows with every argument,
+  // but the rows kernel has eight workers per CTA where the tiles kernel has one,
+  // so its largest call can need more than the tiles kernel's smallest: the larger
+  // of the two counts.
   AttnArgs g = {};
   Need n = plan(g, T, B, max_q, hq, hkv, D, prefix_len, true, kMaxCtas);
-  const int G = hq / hkv;
-  if (G <= kPrefixRows) {
-    const Slots p = plan(g = {}, std::min(T, kPrefixRows / G), B, max_q, hq, hkv, D, prefix_len, true,
-                         kMaxCtas).prefix;
-    const Slots o = plan(g = {}, T, B, std::min(max_q, kOwnRows / G), hq, hkv, D, prefix_len, true,
+  const int tokens = most_rows(D) / (hq / hkv);
+  if (tokens > 0) {
+    const Slots p = plan(g = {}, std::min(T, tokens), B, max_q, hq, hkv, D,
+                         std::min(prefix_len, kPrefixOf32), true, kMaxCtas).prefix;
+    const Slots o = plan(g = {}, T, B, std::min(max_q, tokens), hq, hkv, D, prefix_len, true,
                          kMaxCtas).own;
     n.prefix = {std::max(n.prefix.units, p.units), std::max(n.prefix.rows, p.rows)};
     n.own = {std::max(n.own.units, o.units), std::max(n.own.rows, o.rows)};

@@ -1,8 +1,8 @@
 // prefix_attention_rows.cu -- shared-prefix attention for few query rows.
 //
-// With up to 32 rows (tokens x query heads of a key head) per unit the work
-// is reading keys and values: at D = 128 a slice of 16 keys is 8 KB and 32
-// (64) small MMAs.  So every warp works for itself: it owns a piece of the
+// With up to 16 rows (tokens x query heads of a key head) per unit, or 32 at D =
+// 64, the work is reading keys and values: at D = 128 a slice of 16 keys is 8 KB
+// and 32 small MMAs.  So every warp works for itself: it owns a piece of the
 // line, streams its slices through a private ring in shared memory
 // (cp.async, the next slices always in flight), and keeps queries, scores,
 // probabilities and accumulators in registers (mma.sync m16n8k16, which a
@@ -355,10 +355,11 @@ cudaError_t run(const AttnArgs &g, int ctas, cudaStream_t s) {
 
 template <int DTYPE, int D>
 cudaError_t run_d(const AttnArgs &g, int ctas, cudaStream_t s) {
-  if (g.share && g.a.B <= 128)
-    return g.r_mt == 1 ? run<DTYPE, D, 1, 2>(g, ctas, s) : run<DTYPE, D, 2, 2>(g, ctas, s);
-  return g.r_mt == 1 ? run<DTYPE, D, 1, kRowWarps>(g, ctas, s)
-                     : run<DTYPE, D, 2, kRowWarps>(g, ctas, s);
+  const bool small = g.share && g.a.B <= 128;
+  if constexpr (D == 64)  // 16 rows are the most at D = 128
+    if (g.r_mt == 2)
+      return small ? run<DTYPE, D, 2, 2>(g, ctas, s) : run<DTYPE, D, 2, kRowWarps>(g, ctas, s);
+  return small ? run<DTYPE, D, 1, 2>(g, ctas, s) : run<DTYPE, D, 1, kRowWarps>(g, ctas, s);
 }
 
 }  // namespace

@@ -92,3 +92,23 @@ def test_ragged_queries_at_head_size_128(G, prefix, dtype):
 def test_a_prompt_over_its_own_rows(n, own, D, dtype):
     # one sequence and its causal triangle; with rows before it; with tokens that see nothing
     Case([n], [own], 0, hq=16, hkv=2, D=D, dtype=dtype, page=32).check()
+
+
+@pytest.mark.parametrize("D,dtype", FORMS)
+@pytest.mark.parametrize("n,G", [(15, 1), (16, 1), (17, 1), (8, 2), (9, 2), (31, 1), (32, 1), (33, 1), (1, 16),
+                                 (1, 17), (1, 32), (1, 33), (4, 8), (5, 8)])
+@pytest.mark.parametrize("prefix", [0, 200, 4096, 4097])
+def test_row_counts_where_the_kernel_changes(n, G, D, dtype, prefix):
+    # of the sequence, and of the batch over the prefix
+    Case([n], [max(n, 150)], prefix, hq=2 * G, hkv=2, D=D, dtype=dtype, page=64).check()
+    Case([1] * n, [20 + 9 * b for b in range(n)], prefix, hq=G, hkv=1, D=D, dtype=dtype, page=64).check()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, FP16), (128, BF16)])
+@pytest.mark.parametrize("B,prefix,own", [(3, 128, 5000), (128, 1000, 40), (129, 40, 190), (300, 257, 20),
+                                          (700, 129, 33)])
+def test_prefix_tiles_beside_own_rows_of_16(B, prefix, own, D, dtype):
+    # few and many sequences, either part the longer one, 16 rows of each sequence
+    lens = [own - (11 * b) % (own // 2 + 1) for b in range(B)]
+    lens[B // 2] = 0
+    Case([1] * B, lens, prefix, hq=16, hkv=1, D=D, dtype=dtype, page=16).check()
