@@ -82,7 +82,7 @@ moe_status_t check_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, in
   if (T < 0 || num_seqs < 0 || max_q < 1 || prefix_len < 0 || prefix_len > kMostKeys)
     return MOE_ERR_INVALID_ARG;
   if (num_seqs > 4096) return MOE_ERR_UNSUPPORTED;
-  // the partial results are indexed with 32-bit row numbers
+  // units (blocks of tokens x key heads, at most T x heads of them) are counted in int
   if (static_cast<int64_t>(T) * kv->num_q_heads >= (int64_t{1} << 30)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

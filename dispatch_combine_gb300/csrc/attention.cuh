@@ -187,9 +187,10 @@ __device__ __forceinline__ OwnScan scan_own(const AttnArgs &g, ScanShared<THREAD
 // own row each over a prefix of 1024 took 26.2 us without it, 22.8 with it).
 //   sm_rate 60, 70, 80 GB/s at D = 128: 64 sequences, prefix 8192, own rows up
 // to 1024: 53.8, 51.7, 49.7 us; 64, 2048 and 4096: 115.7, 115.6, 120.2; 128,
-// 8192 and 512: 67.8, 65.8, 65.3.  45, 55, 65 at D = 64: 37 drafts, 20000 and
-// 777: 52.6, 52.7, 61.8; 100, 4099 and 2000: 47.6, 49.5, 52.9.  Without
-// rows_us0: 37 drafts, 4099 and 777: 33.4 instead of 29.1.
+// 8192 and 512: 67.8, 65.8, 65.3.  45 and 55 at D = 64 (4 key heads of 7): 64 of
+// up to 4 tokens, 4099 and 777: 29.1, 34.6; 100, 4099 and 2000: 36.9, 34.6.
+// Without rows_us0, D = 64: the former 34.7, 32 of up to 2 tokens (8 heads of 8),
+// 1000 and 300: 26.9 instead of 20.6; D = 128: 64, 8192 and 1024: 49.3, 52.9 with.
 struct ShareOut {
   int gangs, workers;
 };
@@ -371,10 +372,16 @@ __device__ __forceinline__ float ex2(float x) {
 // rounding cancels as long as the sums are rescaled by, and the log-sum-exp taken
 // from, this number.  It must not carry a probability past its type: up to
 // kMost it rounds by at most 1/2 (2^15.5) or 32 (2^40).  Past it a row's result
-// is NaN (taking the maximum off the scores first has no such end, but as one
+// is NaN.  (Taking the maximum off the scores first has no such end, but as one
 // more addition per score, or a branch around the exponentials for such rows
 // alone, 256 queries over 32768 rows took 231 to 255 us at head size 128
-// instead of 212).
+// instead of 212.)
+// They are rounded to the cache's type for the product with V, the one rounding
+// to 16 bits before the output's: the tensor cores take both operands in one
+// type, and in two parts (high and low) the products would double.  It makes the
+// output's error against 64 bits 1.2 to 1.4 times that of the output's own
+// rounding (bf16 0.0020 to 0.0023 relative, 0.0017 without; fp16 0.00027 and
+// 0.00021).  The sum is taken of the unrounded ones.
 template <int DTYPE>
 struct Prob {
   static constexpr float kOff = DTYPE == MOE_DTYPE_FP16 ? 10.0f : 0.0f;

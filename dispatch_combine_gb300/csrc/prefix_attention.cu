@@ -7,10 +7,10 @@
 // lse = log sum p, and parts join with weights exp(lse - max lse).
 //
 // The prefix is read once for the whole batch (a block of tokens of all
-// sequences is one set of query rows), each sequence's own rows once for the
-// sequence.  Few rows per key head (the common decode step) go to the rows
-// kernel, which is made to stream the cache; many go to the tiles kernel,
-// which is made to feed the tensor cores.  A call that needs both runs them
+// sequences is one set of query rows), each sequence's own rows once for each
+// block of its tokens (up to 256 rows).  Few rows per key head (the common
+// decode step) go to the rows kernel, which is made to stream the cache; many
+// go to the tiles kernel, which is made to feed the tensor cores.  A call that needs both runs them
 // side by side: the tiles kernel uses as many SMs as lets both end together
 // (it reads the lengths on the device), and the rows kernel, launched behind it
 // without waiting for it, starts on the others (64 sequences, prefix 8192, own

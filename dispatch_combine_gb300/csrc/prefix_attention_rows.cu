@@ -24,10 +24,10 @@ namespace moe {
 namespace {
 
 // WARPS per CTA: 8, or 2 beside the tiles kernel for a small batch, where a
-// small CTA starts sooner (37 sequences over a prefix of 128: 16.1 us, 18.1 with
-// 8).  Every CTA reads the batch's lengths once, so large batches want large
-// CTAs (4096 sequences of up to 512 over 1024, 16 + 2 heads: 318 and 285 us);
-// from 64 to 256 sequences the two are within 1 us.
+// small CTA starts sooner (37 tokens, 4 key heads of 7 at D = 64, prefix 128, own
+// rows up to 777: 17.2 us, 18.4 with 8).  Every CTA reads the batch's lengths
+// once, so large batches want large CTAs (4096 sequences of up to 512 over 1024,
+// 16 + 2 heads: 318 and 285 us); from 64 to 256 sequences the two are within 1 us.
 template <int D, int WARPS>
 struct RowCfg {
   static constexpr int SLICE = kSlice * D * 2;     // bytes of K or of V

@@ -18,7 +18,7 @@
 //
 // Bound by the tensor cores (4 D flop per score): a tile of a wide unit is 32
 // products of 128 x 128 x 16 per SM at 64 cycles.  256 queries x 64 heads of
-// 128 over 131072 rows (1.10 PFLOP) take 755 us, 0.75 of the measured bf16
+// 128 over 131072 rows (1.10 TFLOP) take 755 us, 0.75 of the measured bf16
 // peak; the MMAs alone would take 570, the softmax alone 545.
 #include <algorithm>
 #include <cstddef>

@@ -102,9 +102,9 @@ moe_status_t moe_expert_ffn_workspace_size(const moe_shape_t *shape, int32_t lay
                                            int32_t M_max, size_t *bytes);
 
 /* Prepares a fresh workspace (async): clears the device status word and the
- * flags the expert FFN's down GEMM uses between CTAs (zero at rest, and left
- * zero by every call that completes).  Call once before the workspace's
- * first use. */
+ * flags the expert FFN's down GEMM uses between CTAs (every call that uses
+ * them clears them first, so calls of one stream may share a workspace).  Call
+ * once before the workspace's first use. */
 moe_status_t moe_workspace_init(void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Synchronises `stream`, returns the OR of device-side errors recorded in the
@@ -561,8 +561,9 @@ typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_PAIRS = 1 } moe_rope_t;
  *   (rot_dim % 16 == 0, 0 <= rot_dim <= head_dim), the rest is copied;
  *   q_out [T, num_q_heads, head_dim] with its token stride; may be q (same
  *   stride); q NULL: keys and values only.
- * The angle is reduced in fp64 (exact to 1e-7 turns up to 2^31 positions),
- * sine, cosine and the rotation are fp32, one rounding at the end.
+ * The angle is reduced in fp64 (to 1.2e-7 of a turn at 2^31 positions, 6e-11 at
+ * 10^6, then rounded to 24 bits), sine, cosine and the rotation are fp32, one
+ * rounding at the end.
  * A slot outside [-1, num_pages * page_size) is skipped and reported as
  * MOE_ERR_INVALID_ARG in the workspace's status word (ws of at least 256
  * bytes; NULL: not reported).  Slots must be distinct: of two tokens with one
@@ -595,8 +596,9 @@ moe_status_t moe_kv_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t
  *   A token that sees nothing gets zeros and -inf; a head whose query holds a
  *   NaN or an infinity, or whose largest score passes 1.1e7 (fp16) or 7e8 (bf16)
  *   in magnitude, gets NaN in both.
- *   scores are scale * q.k (scale > 0, finite); softmax statistics and sums are fp32, the
- *   probabilities are rounded to the cache's type for the product with V.
+ *   scores are scale * q.k (scale > 0, finite); softmax statistics and sums are
+ *   fp32, the probabilities are rounded to the cache's type for the product
+ *   with V.
  * What lies in pages past kv_lens or past the prefix's end is never used,
  * whatever it holds; the rows below kv_lens must be finite.
  * Errors on the device: a page id outside [0, num_pages), kv_lens negative or
