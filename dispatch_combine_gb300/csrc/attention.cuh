@@ -397,16 +397,23 @@ template <int DTYPE>
 __device__ __forceinline__ float rescale(float m, float m1, float sl2) {
   return m == -INFINITY ? 0.0f : ex2(prob_offset<DTYPE>(m1, sl2) - prob_offset<DTYPE>(m, sl2));
 }
+// The maximum to take for scores up to `top`: none below the range, so that
+// scores down there have probabilities of 0 and not of their type's infinity.
+template <int DTYPE>
+__device__ __forceinline__ float in_range(float top, float sl2) {
+  return fmaxf(top, -Prob<DTYPE>::kMost / sl2);
+}
 // A part's scale and log2-sum-exp from its sum l: 0 and -infinity where it saw
-// nothing; a NaN (a query that is not finite, scores past the range) stays one.
+// nothing, or only scores below the range; a NaN (a query that is not finite,
+// scores above the range) stays one.
 struct PartEnd {
   float inv, lse;
 };
 template <int DTYPE>
 __device__ __forceinline__ PartEnd end_part(float m, float l, float sl2) {
   const float c0 = prob_offset<DTYPE>(m, sl2);
+  if (c0 < -Prob<DTYPE>::kMost) l = NAN;
   if (l == 0.0f) return {0.0f, -INFINITY};
-  if (fabsf(c0) > Prob<DTYPE>::kMost) l = NAN;
   return {1.0f / l, log2f(l) - c0};
 }
 constexpr float kLog2e = 1.4426950408889634f;

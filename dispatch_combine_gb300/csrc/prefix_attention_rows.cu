@@ -207,6 +207,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int6
                             fmaxf(sc[m][1][2 * h], sc[m][1][2 * h + 1]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = in_range<DTYPE>(top, sl2);
           if (top > mx[m][h]) {
             const float f = rescale<DTYPE>(mx[m][h], top, sl2);
             mx[m][h] = top;

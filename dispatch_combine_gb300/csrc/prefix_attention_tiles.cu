@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (rare(__any_sync(0xffffffffu, moves))) {
           if (!last_product()) break;
           waited = true;
-          const float m1 = moves ? top : m;
+          const float m1 = moves ? in_range<DTYPE>(top, sl2) : m;
           const float f = moves ? rescale<DTYPE>(m, m1, sl2) : 1.0f;
           m = m1;
           const float2 lv = unpack_f32x2(l2);

@@ -8,6 +8,7 @@ import torch
 
 import dispatch_combine_gb300 as moe
 from tests.gpu_common import ensure_lib
+from tests.test_gpu_attention_tiles import LONG, long_case
 from tests.test_gpu_prefix_attention import BF16, FP16, Case
 
 pytestmark = pytest.mark.gpu
@@ -142,3 +143,25 @@ def test_large_scores_that_rise_a_little(D, dtype, G, T, n):
     assert ((o.double() - ro).abs() <= half * ro.abs() + (half + 2e-4) * 1.01 * ra).all()
     want = 2.0 ** 22 + math.log(n - 1 + math.exp(6.0))
     assert ((lse.double() - want).abs() <= 2.0 ** -21 * want).all()
+
+
+@pytest.mark.parametrize("name", list(ROUTES) + list(LONG))
+@pytest.mark.parametrize("D,dtype", FORMS)
+@pytest.mark.parametrize("scale", [2.0 ** -8, 4.0, 2.0 ** 60])
+@pytest.mark.parametrize("where", ["first", "prefix"])
+def test_keys_far_below_the_others_weigh_nothing(name, D, dtype, scale, where):
+    # scores of -2^30 * scale for the first third of the keys, or all of the
+    # prefix's; of the others' as usual
+    c = route(name, D, dtype) if name in ROUTES else long_case(name, D, dtype)
+    if where == "prefix" and (not c.prefix or min(c.lens_list) == 0):
+        pytest.skip("no token sees other keys")
+    c.q = (c.q.double() * (D ** -0.5 / scale)).to(torch.float32)
+    c.q = c.q.clamp(-2.0, 2.0).to(dtype)
+    c.q[..., 3] = 2.0 ** 15
+    for i, (pages, n) in enumerate([(c.prefix_pages, c.prefix)] + list(zip(c.table, c.lens_list))):
+        far = n // 3 if where == "first" else n if i == 0 else 0
+        for j in range(-(-n // c.page)):
+            m = min(c.page, n - j * c.page)
+            low = (torch.arange(m, device="cuda") + j * c.page < far).to(dtype)
+            c.k[pages[j].long(), :, :m, 3] = low * -2.0 ** 15
+    c.check(got=c.run(scale=scale), scale=scale)
