@@ -25,6 +25,7 @@ MOE_LAYOUT_CONTIGUOUS = 0
 MOE_LAYOUT_MASKED = 1
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_FP16 = 1
+MOE_DTYPE_FP32 = 2
 MOE_NORM_RMS = 0
 MOE_NORM_LAYER = 1
 MOE_GATE_NONE = 0
@@ -125,6 +126,15 @@ SIGNATURES = {
                                                    ctypes.POINTER(_SZ)]),
     "moe_prefix_attention": (_I32, [_PK, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _P, _I32, _P,
                                     _I32, _P, _F32, _P, _I64, _P, _P, _SZ, _P]),
+    "moe_kv4_page_bytes": (_SZ, [_PK]),
+    "moe_kv4_append": (_I32, [_PK, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _I32, _P,
+                              _P, _P, _I64, _P, _SZ, _P]),
+    "moe_kv4_read": (_I32, [_PK, _I32, _P, _P, _P, _P, _I32, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "moe_kv4_attention_workspace_size": (_I32, [_PK, _I32, _I32, _I32, ctypes.POINTER(_SZ)]),
+    "moe_kv4_attention": (_I32, [_PK, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _P, _I32, _P, _F32,
+                                 _P, _I64, _P, _P, _SZ, _P]),
+    "moe_verify_drafts": (_I32, [_I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _P,
+                                 _P, _SZ, _P]),
     "moe_selftest_wait_timeout": (_I32, [_P, _SZ, _U64, _P]),
 }
 
@@ -862,11 +872,9 @@ def _kv_dtype(kv):
     return torch.bfloat16 if kv.dtype == MOE_DTYPE_BF16 else torch.float16
 
 
-def moe_kv_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cache,
-                  ws: Workspace = None, style=MOE_ROPE_HALF, q_out=None, stream=None):
-    """Rotate q [T, Hq, D] (returned, or None when q is None) and k [T, Hkv,
-    D] by their positions and append k and v to the cache at `slots`.  The
-    first 2 * len(inv_freq) elements of each head turn (inv_freq None: none)."""
+def _append(name, kv, cache_dtype, cache_shape, q, k, v, positions, slots, inv_freq, k_cache,
+            v_cache, ws, style, q_out, stream):
+    """Both appends: only the form of the cache differs."""
     dt = _kv_dtype(kv)
     T, D, hkv = k.shape[0], kv.head_dim, kv.num_kv_heads
     qp, qs, qo, qos = None, 0, None, 0
@@ -886,15 +894,24 @@ def moe_kv_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cac
         rot = 2 * inv_freq.numel()
         fp = _dense(inv_freq, torch.float32, (rot // 2,), "inv_freq")
         pp = _dense(positions, torch.int32, (T,), "positions")
-    cache = (kv.num_pages, hkv, kv.page_size, D)
-    _check("moe_kv_append",
-           _fn("moe_kv_append")(ctypes.byref(kv), T, qp, qs, kp, ks, vp, vs, pp,
-                                _dense(slots, torch.int32, (T,), "slots"), fp, rot, style,
-                                _dense(k_cache, dt, cache, "k_cache"),
-                                _dense(v_cache, dt, cache, "v_cache"), qo, qos,
-                                ws.ptr if ws is not None else None,
-                                ws.nbytes if ws is not None else 0, _stream(stream)))
+    _check(name,
+           _fn(name)(ctypes.byref(kv), T, qp, qs, kp, ks, vp, vs, pp,
+                     _dense(slots, torch.int32, (T,), "slots"), fp, rot, style,
+                     _dense(k_cache, cache_dtype, cache_shape, "k_cache"),
+                     _dense(v_cache, cache_dtype, cache_shape, "v_cache"), qo, qos,
+                     ws.ptr if ws is not None else None,
+                     ws.nbytes if ws is not None else 0, _stream(stream)))
     return q_out if q is not None else None
+
+
+def moe_kv_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cache,
+                  ws: Workspace = None, style=MOE_ROPE_HALF, q_out=None, stream=None):
+    """Rotate q [T, Hq, D] (returned, or None when q is None) and k [T, Hkv,
+    D] by their positions and append k and v to the cache at `slots`.  The
+    first 2 * len(inv_freq) elements of each head turn (inv_freq None: none)."""
+    return _append("moe_kv_append", kv, _kv_dtype(kv),
+                   (kv.num_pages, kv.num_kv_heads, kv.page_size, kv.head_dim), q, k, v, positions,
+                   slots, inv_freq, k_cache, v_cache, ws, style, q_out, stream)
 
 
 def moe_prefix_attention_workspace_size(kv: MoeKv, T: int, num_seqs: int, max_q: int,
@@ -948,6 +965,155 @@ def moe_prefix_attention(kv: MoeKv, q, k_cache, v_cache, prefix_pages, prefix_le
                                        _dense(lse, torch.float32, (T, hq), "lse"), ws.ptr,
                                        ws.nbytes, _stream(stream)))
     return out, lse
+
+
+# --------------------------------------------------------------------------
+# serving from a cache held in 4 bits, and drafted tokens
+# --------------------------------------------------------------------------
+
+def _here(*tensors):
+    """The tensors of a call are on the current device, whose stream it runs on."""
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != _current_device():
+            raise ValueError(f"tensor on cuda:{t.get_device()}, not on the current device")
+
+
+def moe_kv4_page_bytes(kv: MoeKv) -> int:
+    """Bytes of one head's rows in one page of a 4-bit cache, which is a uint8
+    tensor [num_pages, num_kv_heads, moe_kv4_page_bytes(kv)]."""
+    n = _fn("moe_kv4_page_bytes")(ctypes.byref(kv))
+    if n == 0:
+        raise MoEError("moe_kv4_page_bytes", 1)
+    return n
+
+
+def _kv4_cache(kv):
+    return kv.num_pages, kv.num_kv_heads, kv.page_size * (kv.head_dim // 2 + kv.head_dim // 16)
+
+
+def moe_kv4_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cache,
+                   ws: Workspace = None, style=MOE_ROPE_HALF, q_out=None, stream=None):
+    """moe_kv_append to a 4-bit cache (see moe_kv4_append in moe.h): k and v are
+    quantised in groups of 32 elements as they are written."""
+    _here(k, v, q, k_cache, v_cache)
+    return _append("moe_kv4_append", kv, torch.uint8, _kv4_cache(kv), q, k, v, positions, slots,
+                   inv_freq, k_cache, v_cache, ws, style, q_out, stream)
+
+
+def moe_kv4_read(kv: MoeKv, slots, k_cache, v_cache, ws: Workspace = None, k_out=None, v_out=None,
+                 dst_slots=None, stream=None):
+    """What the rows at `slots` [n] of a 4-bit cache stand for, in kv's dtype:
+    (k_out, v_out) [n, Hkv, D], or with dst_slots [n] at those rows of the 16-bit
+    caches k_out and v_out [pages, Hkv, page_size, D], which must be given.  A
+    slot of -1 leaves its row as it was (zeros, where the outputs are made here)."""
+    dt = _kv_dtype(kv)
+    n, hkv, D = slots.shape[0], kv.num_kv_heads, kv.head_dim
+    _here(slots, k_cache, v_cache, k_out, v_out, dst_slots)
+    cache = _kv4_cache(kv)
+    dst, pages, ks, vs = None, 0, 0, 0
+    if dst_slots is not None:
+        if k_out is None or v_out is None:
+            raise ValueError("dst_slots: the caches k_out and v_out are missing")
+        dst, pages = _dense(dst_slots, torch.int32, (n,), "dst_slots"), k_out.shape[0]
+        shape = (pages, hkv, kv.page_size, D)
+        kp, vp = _dense(k_out, dt, shape, "k_out"), _dense(v_out, dt, shape, "v_out")
+    else:
+        shape = (n, hkv, D)
+        if k_out is None:
+            k_out = _empty(shape, dt, slots.device, stream)
+            _on(stream, k_out.zero_)
+        if v_out is None:
+            v_out = _empty(shape, dt, slots.device, stream)
+            _on(stream, v_out.zero_)
+        kp, ks = _heads(k_out, dt, shape, "k_out")
+        vp, vs = _heads(v_out, dt, shape, "v_out")
+    _check("moe_kv4_read",
+           _fn("moe_kv4_read")(ctypes.byref(kv), n, _dense(slots, torch.int32, (n,), "slots"),
+                               _dense(k_cache, torch.uint8, cache, "k_cache"),
+                               _dense(v_cache, torch.uint8, cache, "v_cache"), dst, pages, kp, ks,
+                               vp, vs, ws.ptr if ws is not None else None,
+                               ws.nbytes if ws is not None else 0, _stream(stream)))
+    return k_out, v_out
+
+
+def moe_kv4_attention_workspace_size(kv: MoeKv, T: int, num_seqs: int, max_q: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_kv4_attention_workspace_size",
+           lib().moe_kv4_attention_workspace_size(ctypes.byref(kv), int(T), int(num_seqs),
+                                                  int(max_q), ctypes.byref(out)))
+    return out.value
+
+
+def moe_kv4_attention(kv: MoeKv, q, k_cache, v_cache, page_table, kv_lens, ws: Workspace,
+                      q_offsets=None, max_q: int = 1, scale=None, out=None, lse=None,
+                      want_lse=False, stream=None):
+    """Attention of q [T, Hq, D] over each sequence's rows of a 4-bit cache (see
+    moe_kv4_attention in moe.h; scale defaults to D ** -0.5).  Returns (out, lse
+    or None)."""
+    dt = _kv_dtype(kv)
+    T, B, hq = q.shape[0], kv_lens.shape[0], kv.num_q_heads
+    _here(q, k_cache, v_cache, page_table, kv_lens, q_offsets, out, lse)
+    shape = (T, hq, kv.head_dim)
+    qp, qs = _heads(q, dt, shape, "q")
+    if out is None:
+        out = _empty(shape, dt, q.device, stream)
+        op, os_ = out.data_ptr(), hq * shape[2]
+    else:
+        op, os_ = _heads(out, dt, shape, "out")
+    if lse is None and want_lse:
+        lse = _empty((T, hq), torch.float32, q.device, stream)
+    cache = _kv4_cache(kv)
+    max_pages, table = 0, None
+    if page_table is not None:
+        max_pages = page_table.shape[1]
+        table = _dense(page_table, torch.int32, (B, max_pages), "page_table")
+    _check("moe_kv4_attention",
+           _fn("moe_kv4_attention")(ctypes.byref(kv), T, B, max_q, qp, qs,
+                                    _dense(q_offsets, torch.int32, (B + 1,), "q_offsets"),
+                                    _dense(k_cache, torch.uint8, cache, "k_cache"),
+                                    _dense(v_cache, torch.uint8, cache, "v_cache"), table,
+                                    max_pages, _dense(kv_lens, torch.int32, (B,), "kv_lens"),
+                                    kv.head_dim ** -0.5 if scale is None else scale, op, os_,
+                                    _dense(lse, torch.float32, (T, hq), "lse"), ws.ptr, ws.nbytes,
+                                    _stream(stream)))
+    return out, lse
+
+
+_PROB_DTYPES = {torch.float32: MOE_DTYPE_FP32, **_DTYPES}
+
+
+def moe_verify_drafts(target, tokens, uniforms, offsets, draft=None, ws: Workspace = None,
+                      accepted=None, out_tokens=None, stream=None):
+    """Drafted tokens against the target's probabilities (see moe_verify_drafts in
+    moe.h).  target [T, V] and draft (None: drafts taken without a draw) fp32, bf16
+    or fp16, rows dense; tokens [T] int32, uniforms [T] fp32, offsets [B + 1] int32.
+    Returns (accepted [B] int32, out_tokens [T] int32: the drafts that stand, the
+    token after them, -1 behind it)."""
+    if target.dim() != 2:
+        raise ValueError("target: expected [T, V]")
+    shape, dt = target.shape, target.dtype
+    T, V = shape
+    B = offsets.shape[0] - 1
+    if dt not in _PROB_DTYPES:
+        raise TypeError(f"target: expected torch.float32, bfloat16 or float16, got {dt}")
+    _here(target, tokens, uniforms, offsets, draft, accepted, out_tokens)
+    tp, ts = _rows(target, dt, shape, "target")
+    dp, ds = (None, 0) if draft is None else _rows(draft, dt, shape, "draft")
+    if accepted is None:
+        accepted = _empty((B,), torch.int32, target.device, stream)
+    if out_tokens is None:
+        out_tokens = _empty((T,), torch.int32, target.device, stream)
+    row = (T,)
+    _check("moe_verify_drafts",
+           _fn("moe_verify_drafts")(T, B, V, _PROB_DTYPES[dt], tp, ts, dp, ds,
+                                    _dense(tokens, torch.int32, row, "tokens"),
+                                    _dense(uniforms, torch.float32, row, "uniforms"),
+                                    _dense(offsets, torch.int32, (B + 1,), "offsets"),
+                                    _dense(accepted, torch.int32, (B,), "accepted"),
+                                    _dense(out_tokens, torch.int32, row, "out_tokens"),
+                                    ws.ptr if ws is not None else None,
+                                    ws.nbytes if ws is not None else 0, _stream(stream)))
+    return accepted, out_tokens
 
 
 def moe_selftest_wait_timeout(ws: Workspace, limit_ns: int, stream=None):

@@ -1,5 +1,6 @@
 // api_block.cu -- the C ABI of the operators around the layer (norms, cache
-// append, shared-prefix attention): argument validation and launches.
+// append, shared-prefix attention, the 4-bit cache, drafts): argument validation
+// and launches.
 #include <cmath>
 
 #include "common.cuh"
@@ -87,6 +88,109 @@ moe_status_t check_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, in
   return MOE_OK;
 }
 
+// What both appends check, and their arguments for the kernel.
+moe_status_t append_args(const moe_kv_t *kv, int32_t T, const void *q, int64_t q_stride,
+                         const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                         const int32_t *positions, const int32_t *slots, const float *inv_freq,
+                         int32_t rot_dim, int32_t style, void *k_cache, void *v_cache,
+                         void *q_out, int64_t q_out_stride, void *ws, size_t ws_bytes,
+                         moe::KvAppendArgs *out) {
+  MOE_TRY(check_kv(kv));
+  if (T < 0 || rot_dim < 0 || rot_dim > kv->head_dim || rot_dim % 16 != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (style != MOE_ROPE_HALF && style != MOE_ROPE_PAIRS) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const int64_t wq = static_cast<int64_t>(kv->num_q_heads) * kv->head_dim;
+  const int64_t wk = static_cast<int64_t>(kv->num_kv_heads) * kv->head_dim;
+  if (!good_rows(k, k_stride, wk) || !good_rows(v, v_stride, wk) || !slots || !k_cache ||
+      !v_cache || !aligned16(k_cache) || !aligned16(v_cache) || k_cache == v_cache)
+    return MOE_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (q && (!good_rows(q, q_stride, wq) || !good_rows(q_out, q_out_stride, wq) ||
+            (q == q_out && q_stride != q_out_stride)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(slots, 4)) return MOE_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws) MOE_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  moe::KvAppendArgs &a = *out;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.slots = slots;
+  a.inv_freq = inv_freq;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.q_out = q_out;
+  a.q_out_stride = q_out_stride;
+  a.status = static_cast<uint32_t *>(ws);
+  a.T = T;
+  a.hq = kv->num_q_heads;
+  a.hkv = kv->num_kv_heads;
+  a.D = kv->head_dim;
+  a.page_shift = log2_of(kv->page_size);
+  a.rot = rot_dim;
+  a.style = style;
+  a.num_slots = static_cast<int64_t>(kv->num_pages) * kv->page_size;
+  return MOE_OK;
+}
+
+// What both attentions check, and their arguments for the kernels but the
+// workspace.
+moe_status_t attention_args(const moe_kv_t *kv, int32_t T, int32_t num_seqs, int32_t max_q,
+                            const void *q, int64_t q_stride, const int32_t *q_offsets,
+                            const void *k_cache, const void *v_cache, const int32_t *prefix_pages,
+                            int32_t prefix_len, const int32_t *page_table, int32_t max_pages,
+                            const int32_t *kv_lens, float scale, void *o, int64_t o_stride,
+                            float *lse, moe::PrefixAttnArgs *out) {
+  MOE_TRY(check_attention(kv, T, num_seqs, max_q, prefix_len));
+  if (max_pages < 0 || !(scale > 0.0f) || !std::isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_pages) * kv->page_size > kMostKeys)
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!q_offsets && T != num_seqs) return MOE_ERR_INVALID_ARG;
+  const int64_t wq = static_cast<int64_t>(kv->num_q_heads) * kv->head_dim;
+  if (!good_rows(q, q_stride, wq) || !good_rows(o, o_stride, wq) || o == q)
+    return MOE_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!kv_lens || (max_pages > 0 && !page_table))) return MOE_ERR_INVALID_ARG;
+  if (prefix_len > 0 && !prefix_pages) return MOE_ERR_INVALID_ARG;
+  if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(lse, 4) ||
+      (max_pages > 0 && !aligned(page_table, 4)) || (prefix_len > 0 && !aligned(prefix_pages, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if ((prefix_len > 0 || max_pages > 0) &&
+      (kv->num_pages == 0 || !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)))
+    return MOE_ERR_INVALID_ARG;
+  moe::PrefixAttnArgs &a = *out;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.q_offsets = q_offsets;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.prefix_pages = prefix_pages;
+  a.prefix_len = prefix_len;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.kv_lens = kv_lens;
+  a.scale = scale;
+  a.o = o;
+  a.o_stride = o_stride;
+  a.lse = lse;
+  a.T = T;
+  a.B = num_seqs;
+  a.max_q = max_q;
+  a.hq = kv->num_q_heads;
+  a.hkv = kv->num_kv_heads;
+  a.D = kv->head_dim;
+  a.page_shift = log2_of(kv->page_size);
+  a.num_pages = kv->num_pages;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -164,47 +268,9 @@ moe_status_t moe_kv_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t
                            int32_t rot_dim, int32_t style, void *k_cache, void *v_cache,
                            void *q_out, int64_t q_out_stride, void *ws, size_t ws_bytes,
                            moe_stream_t stream) {
-  MOE_TRY(check_kv(kv));
-  if (T < 0 || rot_dim < 0 || rot_dim > kv->head_dim || rot_dim % 16 != 0)
-    return MOE_ERR_INVALID_ARG;
-  if (style != MOE_ROPE_HALF && style != MOE_ROPE_PAIRS) return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;
-  const int64_t wq = static_cast<int64_t>(kv->num_q_heads) * kv->head_dim;
-  const int64_t wk = static_cast<int64_t>(kv->num_kv_heads) * kv->head_dim;
-  if (!good_rows(k, k_stride, wk) || !good_rows(v, v_stride, wk) || !slots || !k_cache ||
-      !v_cache || !aligned16(k_cache) || !aligned16(v_cache) || k_cache == v_cache)
-    return MOE_ERR_INVALID_ARG;
-  if ((q == nullptr) != (q_out == nullptr)) return MOE_ERR_INVALID_ARG;
-  if (q && (!good_rows(q, q_stride, wq) || !good_rows(q_out, q_out_stride, wq) ||
-            (q == q_out && q_stride != q_out_stride)))
-    return MOE_ERR_INVALID_ARG;
-  if (!aligned(slots, 4)) return MOE_ERR_INVALID_ARG;
-  if (rot_dim > 0 && (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 4)))
-    return MOE_ERR_INVALID_ARG;
-  if (ws) MOE_TRY(check_ws(ws, ws_bytes, kStatusBytes));
   moe::KvAppendArgs a = {};
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.positions = positions;
-  a.slots = slots;
-  a.inv_freq = inv_freq;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.q_out = q_out;
-  a.q_out_stride = q_out_stride;
-  a.status = static_cast<uint32_t *>(ws);
-  a.T = T;
-  a.hq = kv->num_q_heads;
-  a.hkv = kv->num_kv_heads;
-  a.D = kv->head_dim;
-  a.page_shift = log2_of(kv->page_size);
-  a.rot = rot_dim;
-  a.style = style;
-  a.num_slots = static_cast<int64_t>(kv->num_pages) * kv->page_size;
+  MOE_TRY(append_args(kv, T, q, q_stride, k, k_stride, v, v_stride, positions, slots, inv_freq,
+                      rot_dim, style, k_cache, v_cache, q_out, q_out_stride, ws, ws_bytes, &a));
   return cuda_status(moe::launch_kv_append(a, kv->dtype, stream));
 }
 
@@ -226,53 +292,140 @@ moe_status_t moe_prefix_attention(const moe_kv_t *kv, int32_t T, int32_t num_seq
                                   const int32_t *page_table, int32_t max_pages,
                                   const int32_t *kv_lens, float scale, void *o, int64_t o_stride,
                                   float *lse, void *ws, size_t ws_bytes, moe_stream_t stream) {
-  MOE_TRY(check_attention(kv, T, num_seqs, max_q, prefix_len));
-  if (max_pages < 0 || !(scale > 0.0f) || !std::isfinite(scale))
-    return MOE_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(max_pages) * kv->page_size > kMostKeys)
-    return MOE_ERR_INVALID_ARG;
+  moe::PrefixAttnArgs a = {};
+  MOE_TRY(attention_args(kv, T, num_seqs, max_q, q, q_stride, q_offsets, k_cache, v_cache,
+                         prefix_pages, prefix_len, page_table, max_pages, kv_lens, scale, o,
+                         o_stride, lse, &a));
   if (T == 0) return MOE_OK;
-  if (!q_offsets && T != num_seqs) return MOE_ERR_INVALID_ARG;
-  const int64_t wq = static_cast<int64_t>(kv->num_q_heads) * kv->head_dim;
-  if (!good_rows(q, q_stride, wq) || !good_rows(o, o_stride, wq) || o == q)
-    return MOE_ERR_INVALID_ARG;
-  if (num_seqs > 0 && (!kv_lens || (max_pages > 0 && !page_table))) return MOE_ERR_INVALID_ARG;
-  if (prefix_len > 0 && !prefix_pages) return MOE_ERR_INVALID_ARG;
-  if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(lse, 4) ||
-      (max_pages > 0 && !aligned(page_table, 4)) || (prefix_len > 0 && !aligned(prefix_pages, 4)))
-    return MOE_ERR_INVALID_ARG;
-  if ((prefix_len > 0 || max_pages > 0) &&
-      (kv->num_pages == 0 || !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)))
-    return MOE_ERR_INVALID_ARG;
   size_t need = 0;
   MOE_TRY(moe_prefix_attention_workspace_size(kv, T, num_seqs, max_q, prefix_len, &need));
   MOE_TRY(check_ws(ws, ws_bytes, need));
-  moe::PrefixAttnArgs a = {};
-  a.q = q;
-  a.q_stride = q_stride;
-  a.q_offsets = q_offsets;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.prefix_pages = prefix_pages;
-  a.prefix_len = prefix_len;
-  a.page_table = page_table;
-  a.max_pages = max_pages;
-  a.kv_lens = kv_lens;
-  a.scale = scale;
-  a.o = o;
-  a.o_stride = o_stride;
-  a.lse = lse;
   a.status = static_cast<uint32_t *>(ws);
   a.scratch = static_cast<uint8_t *>(ws) + kStatusBytes;
-  a.T = T;
-  a.B = num_seqs;
-  a.max_q = max_q;
-  a.hq = kv->num_q_heads;
+  return cuda_status(moe::launch_prefix_attention(a, kv->dtype, stream));
+}
+
+size_t moe_kv4_page_bytes(const moe_kv_t *kv) {
+  if (check_kv(kv) != MOE_OK) return 0;
+  return static_cast<size_t>(kv->page_size) * (kv->head_dim / 2 + kv->head_dim / 16);
+}
+
+moe_status_t moe_kv4_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t q_stride,
+                            const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            const int32_t *positions, const int32_t *slots,
+                            const float *inv_freq, int32_t rot_dim, int32_t style,
+                            void *k_cache, void *v_cache, void *q_out, int64_t q_out_stride,
+                            void *ws, size_t ws_bytes, moe_stream_t stream) {
+  moe::KvAppendArgs a = {};
+  MOE_TRY(append_args(kv, T, q, q_stride, k, k_stride, v, v_stride, positions, slots, inv_freq,
+                      rot_dim, style, k_cache, v_cache, q_out, q_out_stride, ws, ws_bytes, &a));
+  return cuda_status(moe::launch_kv4_append(a, kv->dtype, stream));
+}
+
+moe_status_t moe_kv4_read(const moe_kv_t *kv, int32_t n, const int32_t *slots,
+                          const void *k_cache, const void *v_cache, const int32_t *dst_slots,
+                          int32_t dst_pages, void *k_out, int64_t k_out_stride, void *v_out,
+                          int64_t v_out_stride, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_kv(kv));
+  if (n < 0) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (!slots || !aligned(slots, 4) || !aligned(dst_slots, 4) || !k_cache || !v_cache ||
+      !aligned16(k_cache) || !aligned16(v_cache) || k_out == v_out)
+    return MOE_ERR_INVALID_ARG;
+  const int64_t width = static_cast<int64_t>(kv->num_kv_heads) * kv->head_dim;
+  if (dst_slots) {
+    moe_kv_t dst = *kv;
+    dst.num_pages = dst_pages;
+    MOE_TRY(check_kv(&dst));
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return MOE_ERR_INVALID_ARG;
+  } else if (!good_rows(k_out, k_out_stride, width) || !good_rows(v_out, v_out_stride, width)) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (ws) MOE_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  moe::Kv4ReadArgs a = {};
+  a.k_cache = static_cast<const uint8_t *>(k_cache);
+  a.v_cache = static_cast<const uint8_t *>(v_cache);
+  a.slots = slots;
+  a.dst_slots = dst_slots;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.status = static_cast<uint32_t *>(ws);
+  a.k_stride = k_out_stride;
+  a.v_stride = v_out_stride;
+  a.n = n;
   a.hkv = kv->num_kv_heads;
   a.D = kv->head_dim;
   a.page_shift = log2_of(kv->page_size);
-  a.num_pages = kv->num_pages;
-  return cuda_status(moe::launch_prefix_attention(a, kv->dtype, stream));
+  a.num_slots = static_cast<int64_t>(kv->num_pages) * kv->page_size;
+  a.dst_num_slots = dst_slots ? static_cast<int64_t>(dst_pages) * kv->page_size : 0;
+  return cuda_status(moe::launch_kv4_read(a, kv->dtype, stream));
+}
+
+moe_status_t moe_kv4_attention_workspace_size(const moe_kv_t *kv, int32_t T, int32_t num_seqs,
+                                              int32_t max_q, size_t *bytes) {
+  MOE_TRY(check_attention(kv, T, num_seqs, max_q, 0));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = kStatusBytes + moe::kv4_attention_scratch_bytes(T, num_seqs, max_q, kv->num_q_heads,
+                                                           kv->num_kv_heads, kv->head_dim, true);
+  return MOE_OK;
+}
+
+moe_status_t moe_kv4_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, int32_t max_q,
+                               const void *q, int64_t q_stride, const int32_t *q_offsets,
+                               const void *k_cache, const void *v_cache,
+                               const int32_t *page_table, int32_t max_pages,
+                               const int32_t *kv_lens, float scale, void *o, int64_t o_stride,
+                               float *lse, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  moe::PrefixAttnArgs a = {};
+  MOE_TRY(attention_args(kv, T, num_seqs, max_q, q, q_stride, q_offsets, k_cache, v_cache,
+                         nullptr, 0, page_table, max_pages, kv_lens, scale, o, o_stride, lse, &a));
+  if (T == 0) return MOE_OK;
+  MOE_TRY(check_ws(ws, ws_bytes,
+                   kStatusBytes + moe::kv4_attention_scratch_bytes(
+                                      T, num_seqs, max_q, kv->num_q_heads, kv->num_kv_heads,
+                                      kv->head_dim, false)));
+  a.status = static_cast<uint32_t *>(ws);
+  a.scratch = static_cast<uint8_t *>(ws) + kStatusBytes;
+  return cuda_status(moe::launch_kv4_attention(a, kv->dtype, stream));
+}
+
+moe_status_t moe_verify_drafts(int32_t T, int32_t num_seqs, int32_t vocab, int32_t dtype,
+                               const void *target, int64_t target_stride, const void *draft,
+                               int64_t draft_stride, const int32_t *tokens,
+                               const float *uniforms, const int32_t *offsets, int32_t *accepted,
+                               int32_t *out_tokens, void *ws, size_t ws_bytes,
+                               moe_stream_t stream) {
+  if (T < 0 || num_seqs < 0 || vocab < 1 || vocab > (1 << 30) ||
+      (dtype != MOE_DTYPE_FP32 && !known_dtype(dtype)))
+    return MOE_ERR_INVALID_ARG;
+  if (num_seqs > (1 << 27)) return MOE_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return MOE_OK;
+  const uintptr_t size = dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  if (!offsets || !accepted || !aligned(offsets, 4) || !aligned(accepted, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!target || !aligned(target, size) || target_stride < vocab || !tokens || !uniforms ||
+        !out_tokens || !aligned(tokens, 4) || !aligned(uniforms, 4) || !aligned(out_tokens, 4) ||
+        out_tokens == tokens || accepted == out_tokens || accepted == tokens)
+      return MOE_ERR_INVALID_ARG;
+    if (draft && (!aligned(draft, size) || draft_stride < vocab)) return MOE_ERR_INVALID_ARG;
+  }
+  if (ws) MOE_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  moe::VerifyArgs a = {};
+  a.target = target;
+  a.draft = draft;
+  a.tokens = tokens;
+  a.offsets = offsets;
+  a.uniforms = uniforms;
+  a.accepted = accepted;
+  a.out_tokens = out_tokens;
+  a.status = static_cast<uint32_t *>(ws);
+  a.target_stride = target_stride;
+  a.draft_stride = draft_stride;
+  a.T = T;
+  a.B = num_seqs;
+  a.vocab = vocab;
+  return cuda_status(moe::launch_verify(a, dtype, stream));
 }
 
 }  // extern "C"

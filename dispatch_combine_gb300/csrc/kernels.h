@@ -244,6 +244,31 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs &a, int dtype, cudaStream_t s);
 
+// kv4_append.cu: the cache in 4 bits (kv4.cuh)
+cudaError_t launch_kv4_append(const KvAppendArgs &a, int dtype, cudaStream_t s);
+struct Kv4ReadArgs {
+  const uint8_t *k_cache, *v_cache;
+  const int32_t *slots, *dst_slots;  // dst_slots: into 16-bit caches of dst_num_slots rows
+  void *k_out, *v_out;
+  uint32_t *status;
+  int64_t k_stride, v_stride;        // of the token rows without dst_slots
+  int n, hkv, D, page_shift;
+  int64_t num_slots, dst_num_slots;
+};
+cudaError_t launch_kv4_read(const Kv4ReadArgs &a, int dtype, cudaStream_t s);
+
+// verify.cu
+struct VerifyArgs {
+  const void *target, *draft;  // [T, vocab]; draft nullptr: its tokens had probability 1
+  const int32_t *tokens, *offsets;
+  const float *uniforms;
+  int32_t *accepted, *out_tokens;
+  uint32_t *status;
+  int64_t target_stride, draft_stride;
+  int T, B, vocab;
+};
+cudaError_t launch_verify(const VerifyArgs &a, int dtype, cudaStream_t s);
+
 // prefix_attention.cu
 struct PrefixAttnArgs {
   const void *q, *k_cache, *v_cache;
@@ -259,6 +284,11 @@ struct PrefixAttnArgs {
 size_t prefix_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D,
                                       int prefix_len);
 cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, int dtype, cudaStream_t s);
+
+// kv4_attention.cu (no prefix: prefix_len 0); smaller: enough for every smaller
+// call too
+size_t kv4_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D, bool smaller);
+cudaError_t launch_kv4_attention(const PrefixAttnArgs &a, int dtype, cudaStream_t s);
 
 // api.cu: the shape validation every entry point applies (MOE_OK or an error)
 moe_status_t check_shape_for_abi(const moe_shape_t *shape);

@@ -468,7 +468,11 @@ moe_status_t moe_eplb_plan(const double *load, int32_t num_experts, int32_t num_
  * ------------------------------------------------------------------------ */
 
 /* Element type of activations, weights and caches of these calls. */
-typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1 } moe_dtype_t;
+typedef enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_FP16 = 1,
+  MOE_DTYPE_FP32 = 2 /* probabilities of moe_verify_drafts only */
+} moe_dtype_t;
 
 typedef enum {
   MOE_NORM_RMS = 0,  /* v / sqrt(mean(v^2) + eps) */
@@ -621,6 +625,119 @@ moe_status_t moe_prefix_attention(const moe_kv_t *kv, int32_t T, int32_t num_seq
                                   const int32_t *page_table, int32_t max_pages,
                                   const int32_t *kv_lens, float scale, void *o, int64_t o_stride,
                                   float *lse, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Serving from a cache held in 4 bits: the append that quantises, rows read back
+ * to 16 bits, the attention over it; and the verification of drafted tokens.
+ *
+ * A row of a head is held in groups of 32 elements: a scale s = max|v| / 7
+ * rounded to fp16, and for each element the whole number from -7 to 7 nearest to
+ * v / s (ties to even).  An element stands for its number times s.  A group with
+ * a NaN or an infinity, or whose scale passes fp16 (elements past 458,000),
+ * stands for NaN; one whose scale rounds to zero (elements below 2e-7) for
+ * zeros.  4.5 bits an element: 9/32 of the 16-bit cache.
+ *
+ * k_cache and v_cache are each [num_pages, num_kv_heads, page_bytes] bytes,
+ * page_bytes = moe_kv4_page_bytes(kv) = page_size * (head_dim / 2 + head_dim /
+ * 16): the codes of a page's rows of one head, then their scales.  The order of
+ * the codes in a row is the library's own; moe_kv4_read takes them out.
+ * moe_kv_t and its limits are those of the 16-bit cache; dtype is the type of
+ * queries, of new keys and values and of outputs.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of one head's rows in one page (0 for an invalid descriptor). */
+size_t moe_kv4_page_bytes(const moe_kv_t *kv);
+
+/*
+ * Append T tokens to the 4-bit cache, with the position rotation on the way: the
+ * arguments, checks and errors of moe_kv_append.  Keys are quantised as rotated
+ * in fp32, without a rounding to 16 bits between.
+ */
+moe_status_t moe_kv4_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t q_stride,
+                            const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            const int32_t *positions, const int32_t *slots,
+                            const float *inv_freq, int32_t rot_dim, int32_t style,
+                            void *k_cache, void *v_cache, void *q_out, int64_t q_out_stride,
+                            void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Read n rows back: what the rows at `slots` [n] int32 (page * page_size + row)
+ * stand for, each element rounded once to the dtype.
+ *   dst_slots NULL: row i to k_out / v_out [n, num_kv_heads, head_dim] with their
+ *   token strides (>= num_kv_heads * head_dim, multiples of 8);
+ *   dst_slots [n] int32: to row dst_slots[i] of 16-bit caches k_out / v_out
+ *   [dst_pages, num_kv_heads, page_size, head_dim], as moe_kv_append writes and
+ *   moe_prefix_attention reads them (strides unused; slots must be distinct).
+ * A slot of -1 in either leaves its output row as it was; one outside the cache
+ * too, and is reported as MOE_ERR_INVALID_ARG in the status word (ws as for
+ * moe_kv_append).
+ */
+moe_status_t moe_kv4_read(const moe_kv_t *kv, int32_t n, const int32_t *slots,
+                          const void *k_cache, const void *v_cache, const int32_t *dst_slots,
+                          int32_t dst_pages, void *k_out, int64_t k_out_stride, void *v_out,
+                          int64_t v_out_stride, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Attention over the 4-bit cache: moe_prefix_attention without a prefix, with its
+ * arguments, checks, masks and errors; made for decode (one token, or a few
+ * drafts, for each sequence).  Sequences that share pages name them in each row of
+ * the page table.  A long prefix shared by many sequences, or a long chunk of new
+ * tokens, is better read back into a 16-bit cache (moe_kv4_read) for
+ * moe_prefix_attention.
+ *   The cache's numbers and scales enter the products unrounded; queries are
+ *   held in fp16 after each row's power of two is taken out (elements below 2^-28
+ *   of the row's largest lose bits); the probabilities, and their products with
+ *   the value scales, are rounded to fp16.  A head whose query passes 2^115, or
+ *   holds a NaN or an infinity, or whose largest score passes 1.1e7 in magnitude,
+ *   gets NaN.
+ * Rows below kv_lens must not stand for NaN; what lies past kv_lens is never used.
+ * A workspace sized for some T, num_seqs and max_q (and heads) serves every call
+ * in which none of the three is larger.
+ */
+moe_status_t moe_kv4_attention_workspace_size(const moe_kv_t *kv, int32_t T, int32_t num_seqs,
+                                              int32_t max_q, size_t *bytes);
+moe_status_t moe_kv4_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, int32_t max_q,
+                               const void *q, int64_t q_stride, const int32_t *q_offsets,
+                               const void *k_cache, const void *v_cache,
+                               const int32_t *page_table, int32_t max_pages,
+                               const int32_t *kv_lens, float scale, void *o, int64_t o_stride,
+                               float *lse, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Drafted tokens against the target's probabilities, from given uniform numbers,
+ * so that what is kept is distributed as the target's own samples.
+ *   The rows are the attention's: sequence b holds rows [offsets[b], offsets[b+1])
+ *   (int32 [num_seqs+1]) of new tokens `tokens` [T] int32, the first of them
+ *   already decided and the n others drafts; row i's distribution is that of the
+ *   token after it.
+ *   target [T, vocab] of `dtype` (fp32, bf16 or fp16) with row stride
+ *   target_stride: the target's probabilities; draft likewise: those that token
+ *   i + 1 of the sequence was drawn from in row i (its last row is not read);
+ *   NULL for drafts taken without a draw (probability 1).
+ *   uniforms [T] fp32 in [0, 1): row i's decides on the draft after it, the last
+ *   of a sequence draws its final token.
+ * Draft x after row i stands iff u_i * draft_i(x) < target_i(x) (exactly) and all
+ * drafts before it stand.  accepted [num_seqs] int32: how many do, a.  The token
+ * after them comes from max(target_a - draft_a, 0) (without `draft`: target_a
+ * without x) if a < n, or from target_n: the first token at which the running sum
+ * passes u * the whole.  out_tokens [T] int32: the a drafts that stand, that
+ * token, and -1 behind it.
+ * Differences are rounded to fp32, sums are exact (weights count in units of
+ * 2^-60; a row's should add up to less than 16).  A weight that is NaN or
+ * negative counts as 0, one above 1 as 1.  Where nothing of the difference is
+ * left the token comes from the target's row, where that is all zero it is token 0.
+ * A draft outside [0, vocab) falls and is reported as MOE_ERR_INVALID_ARG in the
+ * status word (ws of at least 256 bytes; NULL: not reported), as are offsets that
+ * decrease or leave [0, T], whose sequences get accepted = 0 and no tokens.  A
+ * sequence without rows gets accepted = 0.
+ * vocab from 1 to 2^30; num_seqs <= 2^27 (MOE_ERR_UNSUPPORTED beyond).
+ */
+moe_status_t moe_verify_drafts(int32_t T, int32_t num_seqs, int32_t vocab, int32_t dtype,
+                               const void *target, int64_t target_stride, const void *draft,
+                               int64_t draft_stride, const int32_t *tokens,
+                               const float *uniforms, const int32_t *offsets, int32_t *accepted,
+                               int32_t *out_tokens, void *ws, size_t ws_bytes,
+                               moe_stream_t stream);
 
 /*
  * Number of kernels moe_layer launches per call for this shape (for launch
