@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(512, 2) kv4_append_kernel(const KvAppendArgs a
   const bool skip = slot < 0 || bad;
   if (bad && threadIdx.x == 0) set_status(a.status, kStatusBadId);
   const int half = a.rot / 2;
-  const int64_t page = slot >> a.page_shift, in_page = slot & ((1 << a.page_shift) - 1);
+  const int64_t page = slot >> a.page_shift;
+  const int in_page = slot & ((1 << a.page_shift) - 1);
   const int64_t page_bytes = static_cast<int64_t>(kv4_row_bytes(a.D)) << a.page_shift;
   bool first = true;
   // (every thread passes the loop once, for the barrier inside; whole warps stay
@@ -178,17 +179,18 @@ __global__ void __launch_bounds__(512, 2) kv4_append_kernel(const KvAppendArgs a
       const int b = c >> 2, part = c & 3;  // group, and eight elements of it
       uint8_t *at = static_cast<uint8_t *>(is_k ? a.k_cache : a.v_cache) +
                     (page * a.hkv + head) * page_bytes;
-      uint8_t *row = at + in_page * kv4_code_bytes(a.D);
       if (is_k) {
-        *reinterpret_cast<uint32_t *>(row + kv4_key_at(a.D, b, part)) = w;
+        *reinterpret_cast<uint32_t *>(at + kv4_key_at(a.D, in_page, b, part)) = w;
       } else {
-        *reinterpret_cast<uint16_t *>(row + kv4_value_at(a.D, b, 2 * part)) = static_cast<uint16_t>(w);
-        *reinterpret_cast<uint16_t *>(row + kv4_value_at(a.D, b, 2 * part + 1)) =
+        *reinterpret_cast<uint16_t *>(at + kv4_value_at(a.D, in_page, b, 2 * part)) =
+            static_cast<uint16_t>(w);
+        *reinterpret_cast<uint16_t *>(at + kv4_value_at(a.D, in_page, b, 2 * part + 1)) =
             static_cast<uint16_t>(w >> 16);
       }
       if (part == 0)
-        *reinterpret_cast<uint16_t *>(at + (static_cast<int64_t>(kv4_code_bytes(a.D)) << a.page_shift) +
-                                      in_page * kv4_scale_bytes(a.D) + 2 * b) = s16;
+        *reinterpret_cast<uint16_t *>(at + (kv4_code_bytes(a.D) << a.page_shift) +
+                                      (is_k ? kv4_key_scale_at(a.D, in_page, b)
+                                            : kv4_value_scale_at(a.D, in_page, b))) = s16;
     }
   }
 }
@@ -219,18 +221,17 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4ReadArgs a) {
     const uint8_t *at = (is_k ? a.k_cache : a.v_cache) +
                         (static_cast<int64_t>(slot >> a.page_shift) * a.hkv + h) * page_bytes;
     const int r = slot & mask;
-    const uint8_t *row = at + static_cast<int64_t>(r) * kv4_code_bytes(a.D);
     uint32_t w;
     if (is_k)
-      w = *reinterpret_cast<const uint32_t *>(row + kv4_key_at(a.D, b, part));
+      w = *reinterpret_cast<const uint32_t *>(at + kv4_key_at(a.D, r, b, part));
     else
-      w = *reinterpret_cast<const uint16_t *>(row + kv4_value_at(a.D, b, 2 * part)) |
+      w = *reinterpret_cast<const uint16_t *>(at + kv4_value_at(a.D, r, b, 2 * part)) |
           static_cast<uint32_t>(
-              *reinterpret_cast<const uint16_t *>(row + kv4_value_at(a.D, b, 2 * part + 1)))
+              *reinterpret_cast<const uint16_t *>(at + kv4_value_at(a.D, r, b, 2 * part + 1)))
               << 16;
     const float s = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(
-        at + (static_cast<int64_t>(kv4_code_bytes(a.D)) << a.page_shift) +
-        static_cast<int64_t>(r) * kv4_scale_bytes(a.D) + 2 * b)));
+        at + (kv4_code_bytes(a.D) << a.page_shift) +
+        (is_k ? kv4_key_scale_at(a.D, r, b) : kv4_value_scale_at(a.D, r, b)))));
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)

@@ -29,6 +29,13 @@
 #include "attention.cuh"
 #include "kv4.cuh"
 
+#ifndef KCENT
+#define KCENT true
+#define INL __forceinline__
+#define W1 12
+#define W2 8
+#define ASMV asm
+#endif
 namespace moe {
 namespace {
 
@@ -46,16 +53,14 @@ constexpr int kMostWarps4 = 16;  // of a CTA
 struct Prob4 {
   static constexpr float kOff = 9.0f, kLag = 5.0f, kMost = 16777216.0f;
 };
-__device__ __forceinline__ float offset4(float m, float sl2, float ev) {
-  return m == -INFINITY ? Prob4::kOff - ev : fmaf(-m, sl2, Prob4::kOff - ev);
-}
 
 template <int D, int WARPS>
 struct Cfg4 {
   static constexpr int NB = D / kGroup4;
-  static constexpr int CODES = Steps4::kKeys * (D / 2);    // bytes of a step's keys or values
-  static constexpr int SCALES = Steps4::kKeys * (D / 16);
-  static constexpr int STAGE = 2 * (CODES + SCALES);
+  static constexpr int CB = kv4_code_bytes(D), SB = kv4_scale_bytes(D);  // of a row
+  static constexpr int CODES = Steps4::kKeys * CB;  // bytes of a step's keys or values
+  static constexpr int SCALES = Steps4::kKeys * SB;
+  static constexpr int STAGE = 2 * (CODES + SCALES);  // key codes, values', key scales, values'
   static constexpr int STAGES = std::min(8, 216 * 1024 / (WARPS * STAGE));
   static constexpr int WARP_BYTES = STAGES * STAGE;
   static constexpr int SMEM_BYTES = WARPS * WARP_BYTES;
@@ -64,6 +69,9 @@ struct Cfg4 {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -75,19 +83,22 @@ __device__ __forceinline__ void cp_async_wait() {
 // N 32-bit words of shared memory
 template <int N>
 __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&v)[N]) {
-  if (N == 4)
+  if constexpr (N == 4)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2 % N]), "=r"(v[3 % N])
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                  : "r"(addr));
-  else if (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1 % N]) : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr));
   else
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr));
+}
+__device__ __forceinline__ void sts_zero16(uint32_t addr) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(0)) : "memory");
 }
 __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                      uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
                                      float c2, float c3) {
-  asm volatile(
+  ASMV(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -95,7 +106,7 @@ __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                      uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  ASMV(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -103,7 +114,7 @@ __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 __device__ __forceinline__ uint32_t transposed8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  ASMV("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -122,34 +133,39 @@ __device__ __forceinline__ float2 half2_at(uint32_t v) {
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // n 2^-24, n 2^-20
 constexpr uint32_t kEight = 0x00080008u, kEightHigh = 0x00800080u;
 
-// where a step's row lies in shared memory among the rows of values: lanes that
-// load together (rows 0, 2, 4, 6 or 1, 3, 5, 7) meet different banks
-__device__ __forceinline__ int value_slot(int r) { return ((r >> 1) & 3) | ((r & 1) << 2) | (r & ~7); }
-
 // One stretch, by one warp.  `slot`: first row of its partial result; `split`:
 // pieces that the query heads of a key head are cut into.
-template <int DTYPE, int D, int NT, int WARPS, bool CENTRED = true>
-__device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int split,
+template <int DTYPE, int D, int NT, int WARPS>
+__device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
                                        int64_t slot, uint32_t ring) {
   using C = Cfg4<D, WARPS>;
   constexpr int NB = C::NB;
   constexpr bool ONCE = DTYPE == MOE_DTYPE_FP16;
+  constexpr bool CENTRED = KCENT || NT > 1;
   const PrefixAttnArgs &a = g.a;
   const int lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
   const int rows = x.ntok * g.G;
-  // ---- the ring.  Lane i keeps the page of the 16 rows `page0 + i`.
+  // ---- the ring.  A step is two runs of 16 rows, each in one page; lane i keeps
+  // the page of run `page0 + i`.
   const int kvh = x.head / split, heads = a.hkv / split;
-  const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
-  const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache);
-  const int spp = a.page_shift - 4;  // log2 of runs of 16 rows per page
-  const int64_t page_bytes = static_cast<int64_t>(kv4_row_bytes(D)) << a.page_shift;
-  const int scales_at = kv4_code_bytes(D) << a.page_shift;
-  const int runs = (x.kv_len + 15) >> 4;
+  const int spp = a.page_shift - 4;  // log2 of runs per page
+  const int page_bytes = kv4_row_bytes(D) << a.page_shift;
+  const int64_t page_stride = static_cast<int64_t>(heads) * page_bytes;
+  const int runs = (x.kv_len + 15) >> 4, run_end = min(runs, 2 * x.s1);
+  constexpr int RC = 16 * C::CB, RS = 16 * C::SB;  // bytes of a run's codes, scales
+  const uint8_t *kl = static_cast<const uint8_t *>(a.k_cache) +
+                      static_cast<int64_t>(kvh) * page_bytes + lane * 16;
+  const uint8_t *vl = static_cast<const uint8_t *>(a.v_cache) +
+                      static_cast<int64_t>(kvh) * page_bytes + lane * 16;
+  // scales: the lanes of a run's keys, of the next run's, then those of values
+  constexpr int SL = RS / 16;
+  const int s_run = (lane / SL) & 1;
+  const uint8_t *sl = (lane < 2 * SL ? kl : vl) + (C::CB << a.page_shift) - (lane / SL) * RS;
   int page0 = 2 * x.s0, page = 0;
   auto fetch_pages = [&](int run) {
     page0 = run;
     page = 0;
-    if (run + lane < min(runs, 2 * x.s1)) {
+    if (run + lane < run_end) {
       page = x.pages[(run + lane) >> spp];
       if (page < 0 || page >= a.num_pages) {
         set_status(a.status, kStatusBadId);
@@ -158,42 +174,30 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
     }
   };
   fetch_pages(page0);
-  auto load = [&](int s) {  // step s into its stage; past the end: an empty group
+  uint32_t into = ring;
+  auto load = [&](int s) {  // past the end: an empty group
     if (s < x.s1) {
-      if (2 * s - page0 >= 32) fetch_pages(2 * s);
-      const int valid = x.kv_len - s * Steps4::kKeys;
-      int64_t base[2];
-      int row[2];  // of the page
+      const int run = 2 * s;
+      if (run - page0 >= 32) fetch_pages(run);
+      const int mask = (1 << spp) - 1;
+      const int64_t at0 = __shfl_sync(0xffffffffu, page, run - page0) * page_stride;
+      const int64_t at1 = __shfl_sync(0xffffffffu, page, run - page0 + 1) * page_stride;
+      const int r0 = run & mask, r1 = (run + 1) & mask;
+      const uint32_t dst = into + lane * 16;
+      const uint32_t n1 = run + 1 < runs ? 16 : 0;  // the second run may be past the end
+      const uint8_t *k0 = kl + at0 + r0 * RC, *k1 = kl + at1 + r1 * RC;
+      const uint8_t *v0 = vl + at0 + r0 * RC, *v1 = vl + at1 + r1 * RC;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t p = __shfl_sync(0xffffffffu, page, 2 * s + h - page0);
-        base[h] = (p * heads + kvh) * page_bytes;
-        row[h] = ((2 * s + h) & ((1 << spp) - 1)) << 4;
+      for (int i = 0; i < RC / 512; ++i) {
+        cp_async16(dst + i * 512, k0 + i * 512);
+        cp_async16(dst + RC + i * 512, k1 + i * 512, n1);
+        cp_async16(dst + C::CODES + i * 512, v0 + i * 512);
+        cp_async16(dst + C::CODES + RC + i * 512, v1 + i * 512, n1);
       }
-      const uint32_t dk = ring + (s - x.s0) % C::STAGES * C::STAGE;
-      const uint32_t dv = dk + C::CODES, ds = dv + C::CODES;
-      constexpr int CH = D / 32;  // 16-byte chunks of a row's codes
-#pragma unroll
-      for (int i = 0; i < C::CODES / 512; ++i) {
-        const int c = i * 32 + lane, r = c / CH, ch = c % CH;
-        const int h = i * 32 / CH >= 16;  // the same for the whole warp
-        const int64_t off = base[h] + (row[h] + (r & 15)) * kv4_code_bytes(D) + ch * 16;
-        const uint32_t n = r < valid ? 16u : 0u;
-        cp_async16(dk + c * 16, kc + off, n);
-        const int vs = value_slot(r);
-        const int vch = D == 128 ? ch ^ (((r >> 2) & 1) * 2) : ch;
-        cp_async16(dv + vs * kv4_code_bytes(D) + vch * 16, vc + off, n);
-      }
-      // scales: rows past the length read as zero
-      constexpr int SR = 16 / kv4_scale_bytes(D);  // rows of a 16-byte chunk
-      constexpr int SN = Steps4::kKeys / SR;       // chunks of keys; then those of values
-      if (lane < 2 * SN) {
-        const int c = lane % SN, r = c * SR, h = r >= 16;
-        const int64_t off =
-            (h ? base[1] : base[0]) + scales_at + ((h ? row[1] : row[0]) + (r & 15)) * kv4_scale_bytes(D);
-        const int n = min(max((valid - r) * kv4_scale_bytes(D), 0), 16);
-        cp_async16(ds + lane * 16, (lane < SN ? kc : vc) + off, n);
-      }
+      if (lane < 4 * SL)
+        cp_async16(dst + 2 * C::CODES, sl + (s_run ? at1 + r1 * RS : at0 + r0 * RS),
+                   s_run ? n1 : 16);
+      into = into + C::STAGE == ring + C::WARP_BYTES ? ring : into + C::STAGE;
     }
     cp_async_commit();
   };
@@ -202,8 +206,11 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
 
   // ---- queries: row r is head r % G of token r / G.  Column gr of block nt.
   uint32_t q[NT][NB][4];
-  float start[NT][NB][2];  // -8 times the group's sum, for the two columns 2t, 2t + 1
-  float sl2[NT][2];
+  // -8 times the groups' sums: the second operand of one more product, with the
+  // groups' scales along the contraction; slots 0 to NB - 1 hold them rounded to
+  // fp16, NB to 2 NB - 1 what that left
+  uint32_t start[NT];
+  uint64_t sl2[NT];        // of the two columns, as everything below
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = nt * 8 + gr, i = r / g.G, hd = r - i * g.G;
@@ -226,6 +233,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
     int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
     e = min(max(e, -24), 100);
     const float down = __uint_as_float((127 - e) << 23);
+    float sums[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float f[8];
@@ -241,182 +249,211 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      sum *= -8.0f / 16777216.0f;
-      start[nt][b][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-      start[nt][b][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+      sums[b] = sum * (-8.0f / 512.0f);  // 2^15 up, away from fp16's subnormals
     }
+    // slots 2t and 2t + 1, of the row itself: column gr
+    const int b0 = (2 * t) % NB;
+    float pair[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      pair[c] = sums[c];
+#pragma unroll
+      for (int b = 2; b < NB; ++b)
+        if (b == b0 + c) pair[c] = sums[b];
+    }
+    const uint32_t high = pack_f16x2(pair[0], pair[1]);
+    const float2 held = half2_at(high);
+    const uint32_t rest = pack_f16x2(pair[0] - held.x, pair[1] - held.y);
+    start[nt] = 2 * t < NB ? high : 2 * t < 2 * NB ? rest : 0u;
     // 2^(e + 24) in two factors
     const float up = a.scale * kLog2e * __uint_as_float((127 + e) << 23) * 16777216.0f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) sl2[nt][c] = __shfl_sync(0xffffffffu, up, 8 * t + 4 * c);
+    sl2[nt] = pack_f32x2(__shfl_sync(0xffffffffu, up, 8 * t),
+                         __shfl_sync(0xffffffffu, up, 8 * t + 4));
   }
 
-  constexpr int ZB = CENTRED ? 1 : NB;
-  float o[NT][NB][2][4], z[NT][ZB][4], mx[NT][2], l[NT][2];
+  float o[NT][NB][2][4], z[NT][CENTRED ? 1 : NB][4];
+  uint64_t c0[NT], l[NT];
   float ev = 0.0f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][b][0][e] = o[nt][b][1][e] = z[nt][b % ZB][e] = 0.0f;
-    mx[nt][0] = mx[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.0f;
+      for (int e = 0; e < 4; ++e) {
+        o[nt][b][0][e] = o[nt][b][1][e] = 0.0f;
+        if (b == 0 || !CENTRED) z[nt][CENTRED ? 0 : b][e] = 0.0f;
+      }
+    c0[nt] = l[nt] = 0;
   }
   const int all_seen = min(x.kv_len, x.lim0);  // keys that every token sees
+  uint32_t from = ring;
 #pragma unroll 1
   for (int s = x.s0; s < x.s1; ++s) {
     cp_async_wait<C::STAGES - 2>();
-    __syncwarp();
-    const uint32_t sk = ring + (s - x.s0) % C::STAGES * C::STAGE;
+    __syncwarp();  // and the stage of the step before is free
+    load(s + C::STAGES - 1);
+    const int key0 = s * Steps4::kKeys;
+    const uint32_t sk = from;
+    from = from + C::STAGE == ring + C::WARP_BYTES ? ring : from + C::STAGE;
     const uint32_t sv = sk + C::CODES, ss = sv + C::CODES;
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const int key0 = s * Steps4::kKeys + half * 16;
-      // ---- scores: keys gr and gr + 8, columns 2t and 2t + 1
-      float sc[NT][4];
-      {
-        uint32_t k0[NB], k1[NB], w0[NB / 2], w1[NB / 2];
-        const uint32_t at = sk + (half * 16 + gr) * kv4_code_bytes(D) + t * (D / 8);
-        lds<NB>(at, k0);
-        lds<NB>(at + 8 * kv4_code_bytes(D), k1);
-        const uint32_t as = ss + (half * 16 + gr) * kv4_scale_bytes(D);
-        lds<NB / 2>(as, w0);
-        lds<NB / 2>(as + 8 * kv4_scale_bytes(D), w1);
+    if (key0 + Steps4::kKeys > x.kv_len) {  // scales past the length: whatever lies there, zero
+      const int r = x.kv_len - key0;
+      if (lane >= r)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float2 p0 = half2_at(w0[b / 2]), p1 = half2_at(w1[b / 2]);
-          const float s0 = b & 1 ? p0.y : p0.x, s1 = b & 1 ? p1.y : p1.x;
-          const uint32_t x0 = k0[b], x1 = k1[b], y0 = x0 >> 8, y1 = x1 >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float d[4];
-            const float *st = start[nt][b];
-            mma4(d, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, q[nt][b][0], q[nt][b][1], st[0],
-                 st[1], st[0], st[1]);
-            mma4(d, y0 & kLow, y1 & kLow, y0 & kHigh, y1 & kHigh, q[nt][b][2], q[nt][b][3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float sb = e < 2 ? s0 : s1;
-              sc[nt][e] = b == 0 ? d[e] * sb : fmaf(d[e], sb, sc[nt][e]);
-            }
-          }
+          sts_zero16(ss + kv4_key_scale_at(D, lane, b));
+          sts_zero16(ss + C::SCALES + kv4_value_scale_at(D, lane, b));
         }
-      }
-      if (key0 + 16 > all_seen) {
+      __syncwarp();
+    }
+    // ---- scores: keys gr and gr + 8 of either half, columns 2t and 2t + 1
+    float sc[2][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+    for (int half = 0; half < 2; ++half) {
+      uint32_t k0[NB], k1[NB], w0[NB / 2], w1[NB / 2];
+      const uint32_t at = sk + (half * 16 + gr) * C::CB + t * (D / 8);
+      lds<NB>(at, k0);
+      lds<NB>(at + 8 * C::CB, k1);
+      const uint32_t as = ss + (half * 16 + gr) * C::SB;
+      lds<NB / 2>(as, w0);
+      lds<NB / 2>(as + 8 * C::SB, w1);
+      const uint32_t a0 = NB == 4 && (t & 1) ? w0[NB / 2 - 1] : w0[0];
+      const uint32_t a1 = NB == 4 && (t & 1) ? w1[NB / 2 - 1] : w1[0];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {  // columns past the rows see everything there is
-            const int r = nt * 8 + 2 * t + c;
-            const int lim = r < rows ? min(x.kv_len, x.lim0 + r / g.G) : x.kv_len;
-            if (key0 + gr >= lim) sc[nt][c] = -INFINITY;
-            if (key0 + gr + 8 >= lim) sc[nt][2 + c] = -INFINITY;
-          }
-      }
-      // ---- value scales: of keys gr (sp[0]) and gr + 8 (sp[1]) where probabilities
-      // take them before they are rounded; else pairs, of keys 2t, 2t + 1 and of
-      // 2t + 8, 2t + 9
-      uint32_t sp[2][ONCE ? NB / 2 : NB];
-      uint32_t any = 0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if constexpr (ONCE) {
-          lds<NB / 2>(ss + C::SCALES + (half * 16 + 8 * k + gr) * kv4_scale_bytes(D), sp[k]);
-#pragma unroll
-          for (int b = 0; b < NB / 2; ++b) any |= sp[k][b];
-        } else {
-          uint32_t w[NB];
-          lds<NB>(ss + C::SCALES + (half * 16 + 8 * k + 2 * t) * kv4_scale_bytes(D), w);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            any |= w[b];
-            sp[k][b] = __byte_perm(w[b / 2], w[NB / 2 + b / 2], b & 1 ? 0x7632 : 0x5410);
-          }
-        }
-      }
-      // ---- the running maximum moves when a score passes it by the lag, and the
-      // exponent of the value scales when one passes it (the test is of the top
-      // bit of fp16 exponents: 2 or more)
-      bool moves = (any & 0x40004000u) != 0;
+      for (int nt = 0; nt < NT; ++nt)
+        mma4(sc[half][nt], a0, a1, 0, 0, start[nt], 0, 0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          moves |= (fmaxf(sc[nt][c], sc[nt][2 + c]) - mx[nt][c]) * sl2[nt][c] > Prob4::kLag;
-      if (__any_sync(0xffffffffu, moves)) {
-        float most = 0.0f;
+        for (int e = 0; e < 4; ++e) sc[half][nt][e] *= 1.0f / 32768.0f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+      for (int b = 0; b < NB; ++b) {
+        const float2 p0 = half2_at(w0[b / 2]), p1 = half2_at(w1[b / 2]);
+        const float s0 = b & 1 ? p0.y : p0.x, s1 = b & 1 ? p1.y : p1.x;
+        const uint32_t x0 = k0[b], x1 = k1[b], y0 = x0 >> 8, y1 = x1 >> 8;
 #pragma unroll
-          for (int b = 0; b < (ONCE ? NB / 2 : NB); ++b) {
-            const float2 p = half2_at(sp[k][b]);
-            most = fmaxf(most, fmaxf(p.x, p.y));
+        for (int nt = 0; nt < NT; ++nt) {
+          float d[4];
+          mma4(d, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, q[nt][b][0], q[nt][b][1], 0.0f,
+               0.0f, 0.0f, 0.0f);
+          mma4(d, y0 & kLow, y1 & kLow, y0 & kHigh, y1 & kHigh, q[nt][b][2], q[nt][b][3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[half][nt][e] = fmaf(d[e], e < 2 ? s0 : s1, sc[half][nt][e]);
+        }
+      }
+    }
+    if (key0 + Steps4::kKeys > all_seen) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // columns past the rows see everything there is
+          const int r = nt * 8 + 2 * t + c;
+          const int lim = (r < rows ? min(x.kv_len, x.lim0 + r / g.G) : x.kv_len) - key0 - gr;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (half * 16 >= lim) sc[half][nt][c] = -INFINITY;
+            if (half * 16 + 8 >= lim) sc[half][nt][2 + c] = -INFINITY;
           }
-        const unsigned top_s = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-        const float ev1 = fmaxf(ev, static_cast<float>(static_cast<int>(top_s >> 23) - 127));
+        }
+    }
+    // ---- exponents.  The running maximum moves when a score passes it by the lag,
+    // and the exponent of the value scales when one passes it (the test is of the
+    // top bit of fp16 exponents: 2 or more).
+    uint64_t ex[2][NT][2];
+    float most = -INFINITY;
+    auto exponents = [&]() {
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(sc[nt][c], sc[nt][2 + c]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, -Prob4::kMost / sl2[nt][c]);
-            // each column by its own scores, so that no head's bits depend on another's
-            const float m = mx[nt][c], m1 = (top - m) * sl2[nt][c] > Prob4::kLag ? top : m;
-            if (m1 > m || ev1 > ev) {
-              const float f = m == -INFINITY
-                                  ? 0.0f
-                                  : ex2(offset4(m1, sl2[nt][c], ev1) - offset4(m, sl2[nt][c], ev));
-              mx[nt][c] = m1;
-              l[nt][c] *= f;
-#pragma unroll
-              for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                  o[nt][b][hh][c] *= f;
-                  o[nt][b][hh][2 + c] *= f;
-                }
-                if (!CENTRED) z[nt][b % ZB][c] *= f;
-              }
-            }
+          for (int r = 0; r < 2; ++r) {
+            ex[half][nt][r] = fma_f32x2(
+                pack_f32x2(sc[half][nt][2 * r], sc[half][nt][2 * r + 1]), sl2[nt], c0[nt]);
+            const float2 f = unpack_f32x2(ex[half][nt][r]);
+            most = fmaxf(most, fmaxf(f.x, f.y));
           }
-        ev = ev1;
+    };
+    exponents();
+    uint32_t any[NB];  // half of the lanes would do
+    lds<NB>(ss + C::SCALES + (lane & 15) * (2 * C::SB), any);
+    uint32_t two = any[0];
+#pragma unroll
+    for (int b = 1; b < NB; ++b) two |= any[b];
+    if (__any_sync(0xffffffffu, most > Prob4::kOff + Prob4::kLag - ev || (two & 0x40004000u) ||
+                                    s == x.s0)) {
+      float big = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float2 p = half2_at(any[b]);
+        big = fmaxf(big, fmaxf(p.x, p.y));
       }
-      // ---- probabilities, as the second operand: keys along the contraction
+      const unsigned top_s = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+      const float ev1 = fmaxf(ev, static_cast<float>(static_cast<int>(top_s >> 23) - 127));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 m = unpack_f32x2(sl2[nt]), was = unpack_f32x2(c0[nt]);
+        float is[2], f[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]),
+                            fmaxf(sc[1][nt][c], sc[1][nt][2 + c]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float u = c ? m.y : m.x, old = c ? was.y : was.x;
+          // each column by its own scores, so that no head's bits depend on another's
+          is[c] = old + (ev - ev1);
+          if (s == x.s0 || fmaf(top, u, old) > Prob4::kOff + Prob4::kLag - ev)
+            is[c] = fmaf(-fmaxf(top, -Prob4::kMost / u), u, Prob4::kOff - ev1);
+          f[c] = ex2(is[c] - old);
+          if (s == x.s0) f[c] = 0.0f;
+        }
+        c0[nt] = pack_f32x2(is[0], is[1]);
+        l[nt] = mul_f32x2(l[nt], pack_f32x2(f[0], f[1]));
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[nt][b][0][e] *= f[e & 1];
+            o[nt][b][1][e] *= f[e & 1];
+            if (!CENTRED) z[nt][CENTRED ? 0 : b][e] *= f[e & 1];
+          }
+      }
+      ev = ev1;
+      exponents();
+    }
+    // ---- probabilities, as the second operand: keys along the contraction
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
       uint32_t p[NT][2];
       float pe[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float(&e)[4] = pe[nt];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float c0 = offset4(mx[nt][c], sl2[nt][c], ev);
-          e[c] = ex2(fmaf(sc[nt][c], sl2[nt][c], c0));
-          e[2 + c] = ex2(fmaf(sc[nt][2 + c], sl2[nt][c], c0));
-          l[nt][c] += e[c] + e[2 + c];
+        for (int r = 0; r < 2; ++r) {
+          const float2 f = unpack_f32x2(ex[half][nt][r]);
+          pe[nt][2 * r] = ex2(f.x);
+          pe[nt][2 * r + 1] = ex2(f.y);
+          l[nt] = add_f32x2(l[nt], pack_f32x2(pe[nt][2 * r], pe[nt][2 * r + 1]));
+          if (!ONCE) p[nt][r] = transposed8x8(pack_f16x2(pe[nt][2 * r], pe[nt][2 * r + 1]));
         }
-        if (!ONCE) {
-          p[nt][0] = transposed8x8(pack_f16x2(e[0], e[1]));
-          p[nt][1] = transposed8x8(pack_f16x2(e[2], e[3]));
-        }
-      }
-      // ---- product with V: elements 4 gr + 2 hh and + 1 of group b, as rows gr
-      // and gr + 8
-      uint32_t v[4][NB / 2];
+      // value scales of pairs: of keys 2t, 2t + 1 and 2t + 8, 2t + 9; where
+      // probabilities take them before they are rounded, those that hold keys gr and
+      // gr + 8
+      uint32_t sp[2][NB];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = half * 16 + 2 * t + (j & 1) + (j >> 1) * 8;
-        const int sw = D == 128 ? ((r >> 2) & 1) * 32 : 0;
-        lds<NB / 2>(sv + value_slot(r) * kv4_code_bytes(D) + ((gr * (D / 16)) ^ sw), v[j]);
-      }
+      for (int k = 0; k < 2; ++k)
+        lds<NB>(ss + C::SCALES + (half * 8 + 4 * k + (ONCE ? gr >> 1 : t)) * (2 * C::SB), sp[k]);
+      // ---- product with V: elements 4 gr + 2 hh and + 1 of group b, as rows gr and
+      // gr + 8; keys 2t, 2t + 1, 2t + 8, 2t + 9 (kv4_value_at)
+      uint32_t v[2][NB];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        lds<NB>(sv + (half * 8 + 4 * j + t) * (2 * C::CB) + kv4_value_turn(D, t, gr * (D / 8)), v[j]);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
-        const uint32_t x0 = __byte_perm(v[0][b / 2], v[1][b / 2], sel), y0 = x0 >> 8;
-        const uint32_t x1 = __byte_perm(v[2][b / 2], v[3][b / 2], sel), y1 = x1 >> 8;
+        const uint32_t x0 = v[0][b], y0 = x0 >> 8, x1 = v[1][b], y1 = x1 >> 8;
         uint32_t f[2][4] = {{x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh},
                             {y0 & kLow, y0 & kHigh, y1 & kLow, y1 & kHigh}};
         if (CENTRED)
@@ -427,8 +464,8 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
         for (int nt = 0; nt < NT; ++nt) {
           uint32_t p0, p1;
           if constexpr (ONCE) {
-            const float2 w0 = half2_at(sp[0][b / 2]), w1 = half2_at(sp[1][b / 2]);
-            const float s0 = b & 1 ? w0.y : w0.x, s1 = b & 1 ? w1.y : w1.x;
+            const float2 w0 = half2_at(sp[0][b]), w1 = half2_at(sp[1][b]);
+            const float s0 = gr & 1 ? w0.y : w0.x, s1 = gr & 1 ? w1.y : w1.x;
             p0 = transposed8x8(pack_f16x2(pe[nt][0] * s0, pe[nt][1] * s0));
             p1 = transposed8x8(pack_f16x2(pe[nt][2] * s1, pe[nt][3] * s1));
           } else {
@@ -438,49 +475,49 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh)
             mma4(o[nt][b][hh], f[hh][0], f[hh][1], f[hh][2], f[hh][3], p0, p1);
-          if (!CENTRED) mma4(z[nt][b % ZB], kEight, kEight, kEight, kEight, p0, p1);
+          if (!CENTRED) mma4(z[nt][CENTRED ? 0 : b], kEight, kEight, kEight, kEight, p0, p1);
         }
       }
     }
-    __syncwarp();  // the stage of this step is free again
-    load(s + C::STAGES - 1);
   }
   cp_async_wait<0>();
   __syncwarp();
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
+    const float2 sums = unpack_f32x2(l[nt]), offs = unpack_f32x2(c0[nt]);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float sum = l[nt][c];
+      float sum = c ? sums.y : sums.x;
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       const int r = nt * 8 + 2 * t + c;
       if (r >= rows) continue;
-      const float c0 = offset4(mx[nt][c], sl2[nt][c], ev);
-      if (c0 < -Prob4::kMost) sum = NAN;
+      const float off = c ? offs.y : offs.x;
+      if (off < -Prob4::kMost) sum = NAN;
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const float low = inv * 16777216.0f, high = inv * 1048576.0f;
       float *dst = g.part_o + (slot + r) * D + 4 * gr;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float off = z[nt][b % ZB][c] * low;
+        const float eight = z[nt][CENTRED ? 0 : b][c] * low;
         *reinterpret_cast<float4 *>(dst + 32 * b) = make_float4(
-            fmaf(o[nt][b][0][c], low, -off), fmaf(o[nt][b][0][2 + c], high, -off),
-            fmaf(o[nt][b][1][c], low, -off), fmaf(o[nt][b][1][2 + c], high, -off));
+            fmaf(o[nt][b][0][c], low, -eight), fmaf(o[nt][b][0][2 + c], high, -eight),
+            fmaf(o[nt][b][1][c], low, -eight), fmaf(o[nt][b][1][2 + c], high, -eight));
       }
-      if (gr == 0) g.part_lse[slot + r] = sum == 0.0f ? -INFINITY : log2f(sum) - c0;
+      if (gr == 0) g.part_lse[slot + r] = sum == 0.0f ? -INFINITY : log2f(sum) - off;
     }
+  }
 }
 
 template <int DTYPE, int D, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 1)
     kv4_attention_kernel(const AttnArgs g, const int split) {
-  pdl_begin();
   using C = Cfg4<D, WARPS>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ ScanShared<WARPS * 32> scan;
   const int warp = threadIdx.x >> 5;
+  pdl_begin();
   const OwnScan own = scan_own<Steps4>(g, scan);
   const int64_t workers = gridDim.x * WARPS;
   const int64_t piece = max(quotient(own.total + workers - 1, workers), static_cast<int64_t>(1));
@@ -548,10 +585,10 @@ cudaError_t run(const AttnArgs &g, int split, int ctas, cudaStream_t s) {
 }
 template <int DTYPE, int D>
 cudaError_t run_d(const AttnArgs &g, const Plan4 &p, int ctas, cudaStream_t s) {
-  if (p.blocks8 == 1) return run<DTYPE, D, 1, 16>(g, p.split, ctas, s);
+  if (p.blocks8 == 1) return run<DTYPE, D, 1, W1>(g, p.split, ctas, s);
   if constexpr (D == 64)
     if (p.blocks8 == 4) return run<DTYPE, D, 4, 8>(g, p.split, ctas, s);
-  return run<DTYPE, D, 2, 8>(g, p.split, ctas, s);
+  return run<DTYPE, D, 2, W2>(g, p.split, ctas, s);
 }
 
 }  // namespace
