@@ -16,20 +16,23 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSlots = 2;  // of a lane on their way while as many are summed
 
 template <int DTYPE>
 __device__ __forceinline__ float prob_at(const void *p, int64_t i) {
   if (DTYPE == MOE_DTYPE_FP32) return static_cast<const float *>(p)[i];
   return load1<DTYPE>(p, i);
 }
-// a weight in [0, 1] in units of 2^-60 (NaN: 0)
+// a weight in [0, 1] in units of 2^-60, cut off
 __device__ __forceinline__ uint64_t units_of(float w) {
-  w = fminf(fmaxf(w, 0.0f), 1.0f);
   const uint32_t b = __float_as_uint(w);
-  const uint64_t m = (b & 0x7FFFFFu) | 0x800000u;
-  const int up = static_cast<int>(b >> 23) - (127 + 23 - 60);
-  if (up >= 0) return m << up;
-  return up > -24 ? m >> -up : 0;
+  const uint32_t high = b << 8 | 0x80000000u;  // the significand at the top of 64 bits
+  const int down = 130 - static_cast<int>(b >> 23);  // 3 and more; 130 for zero
+  const uint32_t low = __funnelshift_rc(0u, high, down);  // as far as 32
+  uint32_t hi, lo;
+  asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(high), "r"(down));  // 0 from 32 on
+  asm("shr.u32 %0, %1, %2;" : "=r"(lo) : "r"(low), "r"(max(down - 32, 0)));
+  return static_cast<uint64_t>(hi) << 32 | lo;
 }
 // floor(u * total) for u in [0, 1), total - 1 past it
 __device__ __forceinline__ uint64_t part_of(float u, uint64_t total) {
@@ -48,10 +51,10 @@ __device__ __forceinline__ uint64_t part_of(float u, uint64_t total) {
 // (j + 1) - m), m what the row's start lies past a 16-byte boundary, so that all
 // slots but the first and the last are one aligned load.
 struct Row {
-  const uint8_t *p, *q;  // of the row; q nullptr: p alone
+  const uint8_t *p, *q;  // of the row, back to the boundary; q nullptr: p alone
   int without;           // token whose weight is 0 (-1: none)
   int vocab, m;
-  bool vectors;          // both rows start alike
+  int full0, full1;      // slots that are one load of each row
 };
 template <int DTYPE>
 constexpr int kVec = DTYPE == MOE_DTYPE_FP32 ? 4 : 8;
@@ -66,37 +69,54 @@ __device__ __forceinline__ void probs(const uint4 &v, float (&f)[kVec<DTYPE>]) {
     unpack8<DTYPE>(v, f);
   }
 }
-// The slots lane, lane + 32, ... (N of them from j0 on): their weights
-template <int DTYPE, int N>
-__device__ __forceinline__ void weights(const Row &r, int j0, int end, int lane,
-                                        uint64_t (&w)[N][kVec<DTYPE>]) {
-  constexpr int V = kVec<DTYPE>, SIZE = 16 / V;
-  float p[N][V], q[N][V];
+// One slot as it lies in memory; zeros where there is nothing, and from `end` on
+template <int DTYPE>
+struct Slot {
+  uint4 p, q;
+  static __device__ __forceinline__ uint32_t word(const uint8_t *row, const Row &r, int64_t at) {
+    constexpr int E = DTYPE == MOE_DTYPE_FP32 ? 1 : 2;  // elements of a word
+    uint32_t w = 0;
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int j = j0 + k * 32 + lane;
-    const int64_t v0 = static_cast<int64_t>(j) * V - r.m;
-    if (r.vectors && j < end && v0 >= 0 && v0 + V <= r.vocab) {
-      probs<DTYPE>(*reinterpret_cast<const uint4 *>(r.p + v0 * SIZE), p[k]);
-      if (r.q) probs<DTYPE>(*reinterpret_cast<const uint4 *>(r.q + v0 * SIZE), q[k]);
+    for (int e = 0; e < E; ++e) {
+      const int64_t i = at + e;
+      if (i < r.m || i - r.m >= r.vocab) continue;
+      if (E == 1)
+        w = reinterpret_cast<const uint32_t *>(row)[i];
+      else
+        w |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[i]) << (16 * e);
+    }
+    return w;
+  }
+  static __device__ __noinline__ uint4 edge(const uint8_t *row, const Row &r, int j) {
+    constexpr int V = kVec<DTYPE>;
+    const int64_t at = static_cast<int64_t>(j) * V;
+    return make_uint4(word(row, r, at), word(row, r, at + V / 4), word(row, r, at + V / 2),
+                      word(row, r, at + 3 * (V / 4)));
+  }
+  __device__ __forceinline__ void load(const Row &r, int j, int end) {
+    p = q = make_uint4(0, 0, 0, 0);
+    if (j >= end) return;
+    if (j >= r.full0 && j < r.full1) {
+      p = *reinterpret_cast<const uint4 *>(r.p + static_cast<int64_t>(j) * 16);
+      if (r.q) q = *reinterpret_cast<const uint4 *>(r.q + static_cast<int64_t>(j) * 16);
     } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int64_t v = v0 + e;
-        const bool in = j < end && v >= 0 && v < r.vocab;
-        p[k][e] = in ? prob_at<DTYPE>(r.p, v) : 0.0f;
-        q[k][e] = in && r.q ? prob_at<DTYPE>(r.q, v) : 0.0f;
-      }
+      p = edge(r.p, r, j);
+      if (r.q) q = edge(r.q, r, j);
     }
   }
+  __device__ __forceinline__ void weights(const Row &r, int j, uint64_t (&w)[kVec<DTYPE>]) const {
+    constexpr int V = kVec<DTYPE>;
+    float x[V], y[V];
+    probs<DTYPE>(p, x);
+    probs<DTYPE>(q, y);
 #pragma unroll
-  for (int k = 0; k < N; ++k)
+    for (int e = 0; e < V; ++e) w[e] = units_of(__saturatef(x[e] - y[e]));
+    if (r.without >= 0 && (r.without + r.m) / V == j)
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int64_t v = static_cast<int64_t>(j0 + k * 32 + lane) * V - r.m + e;
-      w[k][e] = v == r.without ? 0 : units_of(r.q ? p[k][e] - q[k][e] : p[k][e]);
-    }
-}
+      for (int e = 0; e < V; ++e)
+        if ((r.without + r.m) % V == e) w[e] = 0;
+  }
+};
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
   for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -149,20 +169,25 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
   constexpr int V = kVec<DTYPE>;
   const int64_t row = q0 + accepted;
   Row r = {static_cast<const uint8_t *>(a.target) + row * a.target_stride * size, nullptr, -1,
-           a.vocab, 0, true};
-  r.m = static_cast<int>(reinterpret_cast<uintptr_t>(r.p) & 15) / size;
+           a.vocab, 0, 0, 0};
+  bool alike = true;
   if (accepted < n) {
     if (a.draft) {
       r.q = static_cast<const uint8_t *>(a.draft) + row * a.draft_stride * size;
-      r.vectors = ((reinterpret_cast<uintptr_t>(r.p) ^ reinterpret_cast<uintptr_t>(r.q)) & 15) == 0;
+      alike = ((reinterpret_cast<uintptr_t>(r.p) ^ reinterpret_cast<uintptr_t>(r.q)) & 15) == 0;
     } else {
       r.without = fallen;
     }
   }
-  // ---- sums of the warps' parts of the row; a part is 8 pieces of whole warps
+  r.m = alike ? static_cast<int>(reinterpret_cast<uintptr_t>(r.p) & 15) / size : 0;
+  r.p -= r.m * size;
+  if (r.q) r.q -= r.m * size;
+  r.full0 = r.m > 0;
+  r.full1 = alike ? (a.vocab + r.m) / V : 0;
+  // ---- sums of the warps' parts of the row; a part is 8 pieces
   const int slots = (a.vocab + r.m + V - 1) / V;
   const int parts = ctas * kWarps, mine = rank * kWarps + warp;
-  const int piece = ((slots + parts * kWarps - 1) / (parts * kWarps) + 31) / 32 * 32;
+  const int piece = (slots + parts * kWarps - 1) / (parts * kWarps);
   const int64_t part_slots = static_cast<int64_t>(piece) * kWarps;
   const int lo = static_cast<int>(min(mine * part_slots, static_cast<int64_t>(slots)));
   const int hi = static_cast<int>(min((mine + 1) * part_slots, static_cast<int64_t>(slots)));
@@ -171,16 +196,23 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
   uint64_t before = 0;  // it
 #pragma unroll 1
   for (int again = 0; again < 2; ++again) {
-    constexpr int N = 16 / V;  // as many elements in flight with either size
+    constexpr int N = kSlots;
     uint64_t own = 0;
+    Slot<DTYPE> now[N], next[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) now[k].load(r, lo + 32 * k + lane, hi);
 #pragma unroll 1
     for (int j0 = lo; j0 < hi; j0 += 32 * N) {
-      uint64_t w[N][V];
-      weights<DTYPE, N>(r, j0, hi, lane, w);
 #pragma unroll
-      for (int k = 0; k < N; ++k)
+      for (int k = 0; k < N; ++k) next[k].load(r, j0 + 32 * (N + k) + lane, hi);
 #pragma unroll
-        for (int e = 0; e < V; ++e) own += w[k][e];
+      for (int k = 0; k < N; ++k) {
+        uint64_t w[V];
+        now[k].weights(r, j0 + 32 * k + lane, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) own += w[e];
+        now[k] = next[k];
+      }
     }
     __syncwarp();
     own = warp_sum(own);
@@ -197,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
       }
     }
     __syncwarp();
-    cluster_sync_all();  // the sums have been read
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the sums have been read
     const uint64_t first = warp_sum(sum[0]);
     total = first + warp_sum(sum[1]);
     if (total > 0) {
@@ -217,9 +249,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
       before = __shfl_sync(0xffffffffu, upto, owner & 31);
       break;
     }
+    if (again) break;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     r.q = nullptr;  // nothing is left of the difference: the target's own row
     r.without = -1;
-    r.vectors = true;
   }
   // ---- the token: the warps of the owner's CTA take a piece of its part each
   if (owner >= 0 && owner / kWarps == rank) {
@@ -227,13 +260,28 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
     const int64_t from64 = owner * part_slots + static_cast<int64_t>(warp) * piece;
     const int from = static_cast<int>(min(from64, static_cast<int64_t>(end)));
     const int to = min(from + piece, end);
-    uint64_t own = 0;
-#pragma unroll 4
-    for (int j0 = from; j0 < to; j0 += 32) {
-      uint64_t w[1][V];
-      weights<DTYPE, 1>(r, j0, to, lane, w);
+    // the first slots of a lane are kept for the search (all of them up to 64 a piece:
+    // vocabularies of 130000 in fp32, 260000 in 16 bits)
+    constexpr int K = 2;
+    uint64_t w[K][V], sums[K], own = 0;
 #pragma unroll
-      for (int e = 0; e < V; ++e) own += w[0][e];
+    for (int k = 0; k < K; ++k) {
+      Slot<DTYPE> x;
+      x.load(r, from + 32 * k + lane, to);
+      x.weights(r, from + 32 * k + lane, w[k]);
+      sums[k] = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) sums[k] += w[k][e];
+      own += sums[k];
+    }
+#pragma unroll 1
+    for (int j = from + 32 * K + lane; j < to; j += 32) {
+      Slot<DTYPE> x;
+      uint64_t more[V];
+      x.load(r, j, to);
+      x.weights(r, j, more);
+#pragma unroll
+      for (int e = 0; e < V; ++e) own += more[e];
     }
     __syncwarp();
     own = warp_sum(own);
@@ -242,35 +290,42 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
     __syncthreads();
     for (int k = 0; k < warp; ++k) before += s_piece[k];
     if (before <= border && border < before + own) {
-#pragma unroll 1
-      for (int j0 = from; j0 < to; j0 += 32) {
-        uint64_t w[1][V];
-        weights<DTYPE, 1>(r, j0, to, lane, w);
-        __syncwarp();
-        uint64_t mine4 = 0;
-#pragma unroll
-        for (int e = 0; e < V; ++e) mine4 += w[0][e];
-        uint64_t cum = mine4;
+      // whether the border lies in the 32 slots from j on
+      auto search = [&](int j, const uint64_t (&x)[V], uint64_t sum) {
+        uint64_t cum = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const uint64_t up = __shfl_up_sync(0xffffffffu, cum, off);
           if (lane >= off) cum += up;
         }
         const unsigned past = __ballot_sync(0xffffffffu, before + cum > border);
-        if (past) {
-          if (lane == __ffs(past) - 1) {
-            uint64_t sum = before + cum - mine4;
-            int e = 0;
+        if (past && lane == __ffs(past) - 1) {
+          uint64_t upto = before + cum - sum;
+          int e = 0;
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-              sum += w[0][k];
-              e += sum <= border;
-            }
-            a.out_tokens[row] = static_cast<int>(static_cast<int64_t>(j0 + lane) * V - r.m + e);
+          for (int k = 0; k < V; ++k) {
+            upto += x[k];
+            e += upto <= border;
           }
-          break;
+          a.out_tokens[row] = static_cast<int>(static_cast<int64_t>(j + lane) * V - r.m + e);
         }
         before += __shfl_sync(0xffffffffu, cum, 31);
+        return past != 0;
+      };
+      bool found = false;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (!found) found = search(from + 32 * k, w[k], sums[k]);
+#pragma unroll 1
+      for (int j = from + 32 * K; j < to && !found; j += 32) {
+        Slot<DTYPE> x;
+        uint64_t more[V], sum = 0;
+        x.load(r, j + lane, to);
+        x.weights(r, j + lane, more);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum += more[e];
+        __syncwarp();
+        found = search(j, more, sum);
       }
     }
   }
@@ -284,6 +339,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
       if (total == 0) a.out_tokens[row] = 0;
     }
   }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // for the arrival above
 }
 
 template <int DTYPE>
