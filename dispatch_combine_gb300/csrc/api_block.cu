@@ -365,8 +365,8 @@ moe_status_t moe_kv4_attention_workspace_size(const moe_kv_t *kv, int32_t T, int
                                               int32_t max_q, size_t *bytes) {
   MOE_TRY(check_attention(kv, T, num_seqs, max_q, 0));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = kStatusBytes + moe::kv4_attention_scratch_bytes(T, num_seqs, max_q, kv->num_q_heads,
-                                                           kv->num_kv_heads, kv->head_dim, true);
+  *bytes = kStatusBytes + moe::kv4_attention_scratch_bytes(T, max_q, kv->num_q_heads,
+                                                           kv->num_kv_heads, kv->head_dim);
   return MOE_OK;
 }
 
@@ -380,10 +380,9 @@ moe_status_t moe_kv4_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, 
   MOE_TRY(attention_args(kv, T, num_seqs, max_q, q, q_stride, q_offsets, k_cache, v_cache,
                          nullptr, 0, page_table, max_pages, kv_lens, scale, o, o_stride, lse, &a));
   if (T == 0) return MOE_OK;
-  MOE_TRY(check_ws(ws, ws_bytes,
-                   kStatusBytes + moe::kv4_attention_scratch_bytes(
-                                      T, num_seqs, max_q, kv->num_q_heads, kv->num_kv_heads,
-                                      kv->head_dim, false)));
+  size_t need = 0;
+  MOE_TRY(moe_kv4_attention_workspace_size(kv, T, num_seqs, max_q, &need));
+  MOE_TRY(check_ws(ws, ws_bytes, need));
   a.status = static_cast<uint32_t *>(ws);
   a.scratch = static_cast<uint8_t *>(ws) + kStatusBytes;
   return cuda_status(moe::launch_kv4_attention(a, kv->dtype, stream));

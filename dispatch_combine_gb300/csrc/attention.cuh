@@ -65,7 +65,6 @@ struct AttnArgs {
   int own_on, s_wide, s_box;
   OwnPlan own;
   int own_rows_kernel;               // the own rows are the rows kernel's
-  int r_most;                        // the most workers that kernel can have
   SeqMeta *meta;
   // device: the first and the last worker of every unit (prefix units, then
   // own units), written by those two
@@ -429,8 +428,6 @@ constexpr int kTile = TileSteps::kKeys;    // keys per tile
 constexpr int kSlice = SliceSteps::kKeys;  // keys per slice
 constexpr int kMinSlices = 2;   // shortest piece of the rows kernel's line
 
-// prefix_attention.cu: joins the partial results of the call's kernels
-cudaError_t launch_attention_join(const AttnArgs &g, int dtype, int ctas, cudaStream_t s);
 // prefix_attention_rows.cu, prefix_attention_tiles.cu
 cudaError_t launch_attention_rows(const AttnArgs &g, int dtype, int ctas, cudaStream_t s);
 cudaError_t launch_attention_tiles(const AttnArgs &g, int dtype, int ctas, cudaStream_t s);

@@ -285,9 +285,8 @@ size_t prefix_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, 
                                       int prefix_len);
 cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, int dtype, cudaStream_t s);
 
-// kv4_attention.cu (no prefix: prefix_len 0); smaller: enough for every smaller
-// call too
-size_t kv4_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D, bool smaller);
+// kv4_attention.cu (no prefix: prefix_len 0)
+size_t kv4_attention_scratch_bytes(int T, int max_q, int hq, int hkv, int D);
 cudaError_t launch_kv4_attention(const PrefixAttnArgs &a, int dtype, cudaStream_t s);
 
 // api.cu: the shape validation every entry point applies (MOE_OK or an error)

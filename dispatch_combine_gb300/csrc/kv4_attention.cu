@@ -6,15 +6,26 @@
 //   sum_j p_j v_j[d] = sum_j (p_j s_jb) n_jd - 8 sum_j (p_j s_jb),  d in b.
 // The codes go into the matrix instructions as they stand: a nibble alone in its
 // half of a register is the fp16 number n 2^-24 (a subnormal), one nibble further
-// up n 2^-20, so decoding is one AND per two elements.  The powers of two come
-// off the scale of the scores and of the output, the offset of 8 off the
-// accumulators' start (keys) and off one more product with a constant (values).
-// Nothing of the cache is rounded on the way: scales and codes are exact.
+// up n 2^-20, so decoding is one AND per two elements, and the powers of two come
+// off the scale of the scores and of the output.  The offset of 8 comes off the
+// scores in one product of the key's scales with -8 sum q, and off the values' numbers
+// before theirs (exact).  Nothing of the cache is rounded on the way.
 //
 // Keys are the rows (M = 16) of the instruction and query rows its columns (N =
-// 8), so that 8 query heads of a key head, the usual number, fill it.  Every warp
-// is a worker on its own (attention.cuh): it streams steps of 32 keys through a
-// private ring in shared memory (cp.async).
+// 8), so that 8 query heads of a key head, the usual number, fill it.  Units are a
+// sequence's block of tokens x a key head, with up to 16 rows, and stand in a line
+// that is cut into a piece for each warp (attention.cuh): every warp is a worker on
+// its own and streams steps of keys through a private ring in shared memory
+// (cp.async).  A unit that one warp has whole leaves as it should be; of others every
+// warp keeps its part (normalised, with its log-sum-exp), and kv4_join_kernel joins
+// those.
+//
+// Bound by HBM where contexts are long: 16 sequences of up to 131072 rows (8 key heads
+// of 128, 8 query heads each; 1.30 GB) take 202 us, 0.95 of the measured copy
+// bandwidth; without the arithmetic 198.  64 of up to 8192 (364 MB) take 71: 12 us are
+// the two launches, the first rows' way and the join.  Several queries of a sequence
+// are bound by the arithmetic (540 instructions for 32 keys x 8 rows of 128): 37
+// sequences of up to 4099, 6 tokens of 7 heads of 64 each (20 MB) 29 us.
 //
 // Rounded to fewer bits: queries to fp16 after taking out each row's power of two
 // (its largest element is put at 2^14: bf16 ones lose nothing above 2^-28 of it);
@@ -29,23 +40,24 @@
 #include "attention.cuh"
 #include "kv4.cuh"
 
-#ifndef KCENT
-#define KCENT true
-#define INL __forceinline__
-#define W1 12
-#define W2 8
-#define ASMV asm
-#endif
 namespace moe {
 namespace {
 
+// A step is NH runs of 16 keys.  What is done once a step (the copies' addresses,
+// the test for the maximum) is a third of the instructions at 32 keys, and longer
+// straight code fills the waits of the three warps that a scheduler has: 16
+// sequences of up to 131072 rows took 215 us with 32 keys, 202 with 64; two blocks of
+// query rows leave no registers for it (37 sequences, 6 tokens of 7 heads of 64: 29.3
+// and 30.2 us).  A unit costs its start besides: 64 sequences of 8192 rows, 16 query
+// heads each: 112 us counting 2 steps of 32 for it, 105 counting 4.
+template <int NH>
 struct Steps4 {
-  static constexpr int kKeys = 32, kUnitCost = 2;
+  static constexpr int kKeys = 16 * NH, kUnitCost = NH == 4 ? 2 : 4;
   static __device__ __forceinline__ int cost(int) { return 1; }
   static __device__ __forceinline__ int steps_up(int x, int) { return x; }
 };
 
-constexpr int kMostWarps4 = 16;  // of a CTA
+constexpr int kMostWarps4 = 12;  // of a CTA
 
 // Probabilities are 2^(score + c0), c0 = kOff - ev - max, where the value scales
 // are below 2^(ev + 1): 2^(kOff + kLag) at most, and with a scale below 2^15.5.
@@ -54,14 +66,15 @@ struct Prob4 {
   static constexpr float kOff = 9.0f, kLag = 5.0f, kMost = 16777216.0f;
 };
 
-template <int D, int WARPS>
+template <int D, int NH, int WARPS>
 struct Cfg4 {
+  static constexpr int KEYS = 16 * NH;
   static constexpr int NB = D / kGroup4;
   static constexpr int CB = kv4_code_bytes(D), SB = kv4_scale_bytes(D);  // of a row
-  static constexpr int CODES = Steps4::kKeys * CB;  // bytes of a step's keys or values
-  static constexpr int SCALES = Steps4::kKeys * SB;
+  static constexpr int CODES = KEYS * CB;  // bytes of a step's keys or values
+  static constexpr int SCALES = KEYS * SB;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // key codes, values', key scales, values'
-  static constexpr int STAGES = std::min(8, 216 * 1024 / (WARPS * STAGE));
+  static constexpr int STAGES = std::min(8, std::max(2, 170 * 1024 / (WARPS * STAGE)));
   static constexpr int WARP_BYTES = STAGES * STAGE;
   static constexpr int SMEM_BYTES = WARPS * WARP_BYTES;
 };
@@ -69,9 +82,6 @@ struct Cfg4 {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -98,7 +108,7 @@ __device__ __forceinline__ void sts_zero16(uint32_t addr) {
 __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                      uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
                                      float c2, float c3) {
-  ASMV(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -106,7 +116,7 @@ __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                      uint32_t a3, uint32_t b0, uint32_t b1) {
-  ASMV(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -114,7 +124,7 @@ __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 __device__ __forceinline__ uint32_t transposed8x8(uint32_t v) {
   uint32_t r;
-  ASMV("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -133,35 +143,80 @@ __device__ __forceinline__ float2 half2_at(uint32_t v) {
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // n 2^-24, n 2^-20
 constexpr uint32_t kEight = 0x00080008u, kEightHigh = 0x00800080u;
 
-// One stretch, by one warp.  `slot`: first row of its partial result; `split`:
-// pieces that the query heads of a key head are cut into.
-template <int DTYPE, int D, int NT, int WARPS>
-__device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
-                                       int64_t slot, uint32_t ring) {
-  using C = Cfg4<D, WARPS>;
+// Where a token's head goes.
+struct Row4 {
+  uint16_t *o;
+  float *lse;
+};
+template <int D>
+__device__ __forceinline__ Row4 row_at(const PrefixAttnArgs &a, int64_t t, int h) {
+  return {static_cast<uint16_t *>(a.o) + t * a.o_stride + static_cast<int64_t>(h) * D,
+          a.lse ? a.lse + t * a.hq + h : nullptr};
+}
+
+// A unit's normalised rows and their log2-sum-exps from shared memory, by a warp (out
+// of line: the registers of the loop over keys are not these stores'): to a partial
+// result, or to where they belong.
+template <int D>
+__device__ __noinline__ void keep_part(const float *o, const float *lse, float *part, int rows,
+                                       int lse_at) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int i = lane; i < rows * (D / 4); i += 32)
+    *reinterpret_cast<float4 *>(part + 4 * i) = *reinterpret_cast<const float4 *>(o + 4 * i);
+  if (lane < rows) part[lse_at + lane] = lse[lane];
+}
+template <int DTYPE, int D>
+__device__ __noinline__ void write_rows(const AttnArgs &g, const float *o, const float *lse, int tok0,
+                                        int head0, int rows, int lim0, int kv_len) {
+  constexpr int LANES = D / 8;  // of a row
+  const int lane = threadIdx.x & 31, d = lane % LANES * 8;
+#pragma unroll 2
+  for (int r = lane / LANES; r < rows; r += 32 / LANES) {
+    const int i = r * g.tpt >> 16;
+    const Row4 row = row_at<D>(g.a, tok0 + i, head0 + r - i * g.G);
+    float v[8], at = lse[r];
+    *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o + r * D + d);
+    *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(o + r * D + d + 4);
+    // nothing in the sum: zeros, unless keys are seen, all below the range
+    if (at == -INFINITY && min(kv_len, lim0 + i) > 0) {
+      at = NAN;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = NAN;
+    }
+    *reinterpret_cast<uint4 *>(row.o + d) = pack8<DTYPE>(v);
+    if (row.lse && d == 0) *row.lse = at * 0.6931471805599453f;
+  }
+}
+
+// One stretch, by one warp: a whole unit to its rows, else to `part` as a partial
+// result (rows of D, then their log-sum-exps).  `split`: parts that the query heads of
+// a key head are cut into.
+template <int DTYPE, int D, int NT, int NH, int WARPS>
+__device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int split,
+                                       float *part, uint8_t *space) {
+  const uint32_t ring = smem_u32(space);
+  using C = Cfg4<D, NH, WARPS>;
   constexpr int NB = C::NB;
   constexpr bool ONCE = DTYPE == MOE_DTYPE_FP16;
-  constexpr bool CENTRED = KCENT || NT > 1;
   const PrefixAttnArgs &a = g.a;
   const int lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
   const int rows = x.ntok * g.G;
+  // row r is head r % G of token r / G (exact for the few rows there are)
+  auto token_of = [&](int r) { return r * g.tpt >> 16; };
   // ---- the ring.  A step is two runs of 16 rows, each in one page; lane i keeps
   // the page of run `page0 + i`.
   const int kvh = x.head / split, heads = a.hkv / split;
   const int spp = a.page_shift - 4;  // log2 of runs per page
   const int page_bytes = kv4_row_bytes(D) << a.page_shift;
   const int64_t page_stride = static_cast<int64_t>(heads) * page_bytes;
-  const int runs = (x.kv_len + 15) >> 4, run_end = min(runs, 2 * x.s1);
+  const int runs = (x.kv_len + 15) >> 4, run_end = min(runs, NH * x.s1);
   constexpr int RC = 16 * C::CB, RS = 16 * C::SB;  // bytes of a run's codes, scales
-  const uint8_t *kl = static_cast<const uint8_t *>(a.k_cache) +
-                      static_cast<int64_t>(kvh) * page_bytes + lane * 16;
-  const uint8_t *vl = static_cast<const uint8_t *>(a.v_cache) +
-                      static_cast<int64_t>(kvh) * page_bytes + lane * 16;
-  // scales: the lanes of a run's keys, of the next run's, then those of values
-  constexpr int SL = RS / 16;
-  const int s_run = (lane / SL) & 1;
-  const uint8_t *sl = (lane < 2 * SL ? kl : vl) + (C::CB << a.page_shift) - (lane / SL) * RS;
-  int page0 = 2 * x.s0, page = 0;
+  const int64_t head_at = static_cast<int64_t>(kvh) * page_bytes;
+  const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache) + head_at;
+  const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache) + head_at;
+  constexpr int SL = RS / 16;  // lanes that copy a run's scales
+  int page0 = NH * x.s0, page = 0;
   auto fetch_pages = [&](int run) {
     page0 = run;
     page = 0;
@@ -177,26 +232,31 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
   uint32_t into = ring;
   auto load = [&](int s) {  // past the end: an empty group
     if (s < x.s1) {
-      const int run = 2 * s;
+      const int run = NH * s, mask = (1 << spp) - 1;
       if (run - page0 >= 32) fetch_pages(run);
-      const int mask = (1 << spp) - 1;
-      const int64_t at0 = __shfl_sync(0xffffffffu, page, run - page0) * page_stride;
-      const int64_t at1 = __shfl_sync(0xffffffffu, page, run - page0 + 1) * page_stride;
-      const int r0 = run & mask, r1 = (run + 1) & mask;
       const uint32_t dst = into + lane * 16;
-      const uint32_t n1 = run + 1 < runs ? 16 : 0;  // the second run may be past the end
-      const uint8_t *k0 = kl + at0 + r0 * RC, *k1 = kl + at1 + r1 * RC;
-      const uint8_t *v0 = vl + at0 + r0 * RC, *v1 = vl + at1 + r1 * RC;
 #pragma unroll
-      for (int i = 0; i < RC / 512; ++i) {
-        cp_async16(dst + i * 512, k0 + i * 512);
-        cp_async16(dst + RC + i * 512, k1 + i * 512, n1);
-        cp_async16(dst + C::CODES + i * 512, v0 + i * 512);
-        cp_async16(dst + C::CODES + RC + i * 512, v1 + i * 512, n1);
+      for (int j = 0; j < NH; ++j) {
+        const int64_t at = __shfl_sync(0xffffffffu, page, run - page0 + j) * page_stride +
+                           ((run + j) & mask) * RC + lane * 16;
+        const uint32_t n = j == 0 || run + j < runs ? 16 : 0;  // a run may be past the end
+#pragma unroll
+        for (int i = 0; i < RC / 512; ++i) {
+          cp_async16(dst + j * RC + i * 512, kc + at + i * 512, n);
+          cp_async16(dst + C::CODES + j * RC + i * 512, vc + at + i * 512, n);
+        }
       }
-      if (lane < 4 * SL)
-        cp_async16(dst + 2 * C::CODES, sl + (s_run ? at1 + r1 * RS : at0 + r0 * RS),
-                   s_run ? n1 : 16);
+      // scales: the lanes of each run's keys, then those of their values
+#pragma unroll
+      for (int c0 = 0; c0 < 2 * NH * SL; c0 += 32) {
+        const int c = c0 + lane, j = c / SL % NH;
+        const int64_t p = __shfl_sync(0xffffffffu, page, run - page0 + j);
+        if (c < 2 * NH * SL)
+          cp_async16(dst + 2 * C::CODES + c0 * 16,
+                     (c < NH * SL ? kc : vc) + (C::CB << a.page_shift) + p * page_stride +
+                         ((run + j) & mask) * RS + c % SL * 16,
+                     run + j < runs ? 16 : 0);
+      }
       into = into + C::STAGE == ring + C::WARP_BYTES ? ring : into + C::STAGE;
     }
     cp_async_commit();
@@ -204,7 +264,7 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
 #pragma unroll 1
   for (int i = 0; i < C::STAGES - 1; ++i) load(x.s0 + i);
 
-  // ---- queries: row r is head r % G of token r / G.  Column gr of block nt.
+  // ---- queries: row nt * 8 + gr, column gr of block nt
   uint32_t q[NT][NB][4];
   // -8 times the groups' sums: the second operand of one more product, with the
   // groups' scales along the contraction; slots 0 to NB - 1 hold them rounded to
@@ -213,7 +273,7 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
   uint64_t sl2[NT];        // of the two columns, as everything below
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + gr, i = r / g.G, hd = r - i * g.G;
+    const int r = nt * 8 + gr, i = token_of(r), hd = r - i * g.G;
     const bool live = r < rows;
     const uint16_t *src = static_cast<const uint16_t *>(a.q) + (x.tok0 + i) * a.q_stride +
                           (x.head * g.G + hd) * D + 8 * t;
@@ -271,7 +331,7 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
                          __shfl_sync(0xffffffffu, up, 8 * t + 4));
   }
 
-  float o[NT][NB][2][4], z[NT][CENTRED ? 1 : NB][4];
+  float o[NT][NB][2][4];
   uint64_t c0[NT], l[NT];
   float ev = 0.0f;
 #pragma unroll
@@ -279,10 +339,7 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[nt][b][0][e] = o[nt][b][1][e] = 0.0f;
-        if (b == 0 || !CENTRED) z[nt][CENTRED ? 0 : b][e] = 0.0f;
-      }
+      for (int e = 0; e < 4; ++e) o[nt][b][0][e] = o[nt][b][1][e] = 0.0f;
     c0[nt] = l[nt] = 0;
   }
   const int all_seen = min(x.kv_len, x.lim0);  // keys that every token sees
@@ -292,24 +349,23 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
     cp_async_wait<C::STAGES - 2>();
     __syncwarp();  // and the stage of the step before is free
     load(s + C::STAGES - 1);
-    const int key0 = s * Steps4::kKeys;
+    const int key0 = s * C::KEYS;
     const uint32_t sk = from;
     from = from + C::STAGE == ring + C::WARP_BYTES ? ring : from + C::STAGE;
     const uint32_t sv = sk + C::CODES, ss = sv + C::CODES;
-    if (key0 + Steps4::kKeys > x.kv_len) {  // scales past the length: whatever lies there, zero
-      const int r = x.kv_len - key0;
-      if (lane >= r)
+    if (key0 + C::KEYS > x.kv_len) {  // scales past the length: whatever lies there, zero
+      for (int r = x.kv_len - key0 + lane; r < C::KEYS; r += 32)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          sts_zero16(ss + kv4_key_scale_at(D, lane, b));
-          sts_zero16(ss + C::SCALES + kv4_value_scale_at(D, lane, b));
+          sts_zero16(ss + kv4_key_scale_at(D, r, b));
+          sts_zero16(ss + C::SCALES + kv4_value_scale_at(D, r, b));
         }
       __syncwarp();
     }
     // ---- scores: keys gr and gr + 8 of either half, columns 2t and 2t + 1
-    float sc[2][NT][4];
+    float sc[NH][NT][4];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < NH; ++half) {
       uint32_t k0[NB], k1[NB], w0[NB / 2], w1[NB / 2];
       const uint32_t at = sk + (half * 16 + gr) * C::CB + t * (D / 8);
       lds<NB>(at, k0);
@@ -334,23 +390,23 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float d[4];
-          mma4(d, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, q[nt][b][0], q[nt][b][1], 0.0f,
-               0.0f, 0.0f, 0.0f);
-          mma4(d, y0 & kLow, y1 & kLow, y0 & kHigh, y1 & kHigh, q[nt][b][2], q[nt][b][3]);
+          const uint32_t *qb = q[nt][b];
+          mma4(d, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, qb[0], qb[1], 0.0f, 0.0f, 0.0f, 0.0f);
+          mma4(d, y0 & kLow, y1 & kLow, y0 & kHigh, y1 & kHigh, qb[2], qb[3]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[half][nt][e] = fmaf(d[e], e < 2 ? s0 : s1, sc[half][nt][e]);
         }
       }
     }
-    if (key0 + Steps4::kKeys > all_seen) {
+    if (key0 + C::KEYS > all_seen) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {  // columns past the rows see everything there is
           const int r = nt * 8 + 2 * t + c;
-          const int lim = (r < rows ? min(x.kv_len, x.lim0 + r / g.G) : x.kv_len) - key0 - gr;
+          const int lim = (r < rows ? min(x.kv_len, x.lim0 + token_of(r)) : x.kv_len) - key0 - gr;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < NH; ++half) {
             if (half * 16 >= lim) sc[half][nt][c] = -INFINITY;
             if (half * 16 + 8 >= lim) sc[half][nt][2 + c] = -INFINITY;
           }
@@ -359,11 +415,11 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
     // ---- exponents.  The running maximum moves when a score passes it by the lag,
     // and the exponent of the value scales when one passes it (the test is of the
     // top bit of fp16 exponents: 2 or more).
-    uint64_t ex[2][NT][2];
+    uint64_t ex[NH][NT][2];
     float most = -INFINITY;
     auto exponents = [&]() {
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int half = 0; half < NH; ++half)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -375,8 +431,8 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
           }
     };
     exponents();
-    uint32_t any[NB];  // half of the lanes would do
-    lds<NB>(ss + C::SCALES + (lane & 15) * (2 * C::SB), any);
+    uint32_t any[NB];
+    lds<NB>(ss + C::SCALES + lane % (8 * NH) * (2 * C::SB), any);
     uint32_t two = any[0];
 #pragma unroll
     for (int b = 1; b < NB; ++b) two |= any[b];
@@ -396,8 +452,10 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
         float is[2], f[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]),
-                            fmaxf(sc[1][nt][c], sc[1][nt][2 + c]));
+          float top = -INFINITY;
+#pragma unroll
+          for (int half = 0; half < NH; ++half)
+            top = fmaxf(top, fmaxf(sc[half][nt][c], sc[half][nt][2 + c]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -417,7 +475,6 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
           for (int e = 0; e < 4; ++e) {
             o[nt][b][0][e] *= f[e & 1];
             o[nt][b][1][e] *= f[e & 1];
-            if (!CENTRED) z[nt][CENTRED ? 0 : b][e] *= f[e & 1];
           }
       }
       ev = ev1;
@@ -425,7 +482,7 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
     }
     // ---- probabilities, as the second operand: keys along the contraction
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < NH; ++half) {
       uint32_t p[NT][2];
       float pe[NT][4];
 #pragma unroll
@@ -456,10 +513,9 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
         const uint32_t x0 = v[0][b], y0 = x0 >> 8, x1 = v[1][b], y1 = x1 >> 8;
         uint32_t f[2][4] = {{x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh},
                             {y0 & kLow, y0 & kHigh, y1 & kLow, y1 & kHigh}};
-        if (CENTRED)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            f[i / 4][i & 3] = hsub2(f[i / 4][i & 3], i & 1 ? kEightHigh : kEight);
+        for (int i = 0; i < 8; ++i)
+          f[i / 4][i & 3] = hsub2(f[i / 4][i & 3], i & 1 ? kEightHigh : kEight);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           uint32_t p0, p1;
@@ -475,13 +531,15 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh)
             mma4(o[nt][b][hh], f[hh][0], f[hh][1], f[hh][2], f[hh][3], p0, p1);
-          if (!CENTRED) mma4(z[nt][CENTRED ? 0 : b], kEight, kEight, kEight, kEight, p0, p1);
         }
       }
     }
   }
   cp_async_wait<0>();
   __syncwarp();
+  // ---- the rows leave through the ring, where they come to lie in order (and the
+  // accumulators' registers are free for the stores)
+  float *held = reinterpret_cast<float *>(space);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float2 sums = unpack_f32x2(l[nt]), offs = unpack_f32x2(c0[nt]);
@@ -495,112 +553,210 @@ __device__ INL void attend(const AttnArgs &g, const Stretch &x, int split,
       if (r >= rows) continue;
       const float off = c ? offs.y : offs.x;
       if (off < -Prob4::kMost) sum = NAN;
+      const float lse = sum == 0.0f ? -INFINITY : log2f(sum) - off;
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const float low = inv * 16777216.0f, high = inv * 1048576.0f;
-      float *dst = g.part_o + (slot + r) * D + 4 * gr;
+      float *row = held + r * D + 4 * gr;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const float eight = z[nt][CENTRED ? 0 : b][c] * low;
-        *reinterpret_cast<float4 *>(dst + 32 * b) = make_float4(
-            fmaf(o[nt][b][0][c], low, -eight), fmaf(o[nt][b][0][2 + c], high, -eight),
-            fmaf(o[nt][b][1][c], low, -eight), fmaf(o[nt][b][1][2 + c], high, -eight));
-      }
-      if (gr == 0) g.part_lse[slot + r] = sum == 0.0f ? -INFINITY : log2f(sum) - off;
+      for (int b = 0; b < NB; ++b)
+        *reinterpret_cast<float4 *>(row + 32 * b) =
+            make_float4(o[nt][b][0][c] * low, o[nt][b][0][2 + c] * high, o[nt][b][1][c] * low,
+                        o[nt][b][1][2 + c] * high);
+      if (gr == 0) held[8 * NT * D + r] = lse;
     }
   }
+  __syncwarp();
+  if (part)
+    keep_part<D>(held, held + 8 * NT * D, part, rows, g.own.rows * D);
+  else
+    write_rows<DTYPE, D>(g, held, held + 8 * NT * D, x.tok0, x.head * g.G, rows, x.lim0, x.kv_len);
+  __syncwarp();  // before the next stretch's copies
 }
 
-template <int DTYPE, int D, int NT, int WARPS>
+// Tokens that no unit has, of sequences without rows and of no sequence, by a CTA.
+template <int D>
+__device__ __forceinline__ void clear_token(const PrefixAttnArgs &a, int64_t t) {
+  uint4 *row = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + t * a.o_stride);
+  for (int i = threadIdx.x; i < a.hq * (D / 8); i += blockDim.x) row[i] = make_uint4(0, 0, 0, 0);
+  if (a.lse)
+    for (int h = threadIdx.x; h < a.hq; h += blockDim.x) a.lse[t * a.hq + h] = -INFINITY;
+}
+
+// A unit that a worker began and did not end: its parts are the worker's tail part
+// and the head parts of the `parts - 1` workers after it.  (parts 0: there is none.)
+struct Begun {
+  int parts, head, tok0, ntok, lim0, kv_len;
+};
+// A worker has at most two parts: of a unit begun before it, of one that goes on after.
+enum { kTail = 0, kHead = 1 };
+__host__ __device__ constexpr int part_floats(int rows, int D) {  // 16-byte aligned rows
+  return rows * D + (rows + 3) / 4 * 4;
+}
+template <int D>
+__device__ __forceinline__ float *part_at(const AttnArgs &g, int worker, int which) {
+  return g.part_o + static_cast<int64_t>(2 * worker + which) * part_floats(g.own.rows, D);
+}
+
+template <int DTYPE, int D, int NT, int NH, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 1)
-    kv4_attention_kernel(const AttnArgs g, const int split) {
-  using C = Cfg4<D, WARPS>;
+    kv4_attention_kernel(const __grid_constant__ AttnArgs g, const int split, Begun *begun) {
+  using C = Cfg4<D, NH, WARPS>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ ScanShared<WARPS * 32> scan;
-  const int warp = threadIdx.x >> 5;
+  const PrefixAttnArgs &a = g.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // lengths, offsets and page numbers on their way to L2 while the kernels before
+  // this one end (who writes them does it there, too)
+  const int at = blockIdx.x * (WARPS * 32) + threadIdx.x, lines = gridDim.x * (WARPS * 32);
+  auto prefetch = [&](const int32_t *p, int64_t n) {
+    for (int64_t i = at; i * 32 < n; i += lines)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i * 32));
+  };
+  prefetch(a.kv_lens, a.B);
+  if (a.q_offsets) prefetch(a.q_offsets, a.B + 1);
+  prefetch(a.page_table, static_cast<int64_t>(a.B) * a.max_pages);
   pdl_begin();
-  const OwnScan own = scan_own<Steps4>(g, scan);
+  const OwnScan own = scan_own<Steps4<NH>>(g, scan);
+  if (blockIdx.x == 0 && own.bad) set_status(a.status, kStatusBadId);
   const int64_t workers = gridDim.x * WARPS;
   const int64_t piece = max(quotient(own.total + workers - 1, workers), static_cast<int64_t>(1));
-  if (blockIdx.x == 0) write_meta<Steps4>(g, own);
   // consecutive pieces on different SMs
   const int worker = warp * gridDim.x + blockIdx.x;
   const int64_t lo = worker * piece, hi = min(lo + piece, own.total);
-  if (lo >= own.total) return;
-  OwnWalk<Steps4> walk;
-  walk.begin(g, scan, lo, hi);
-  Stretch x;
-  while (walk.next(g, &x)) {
-    if ((threadIdx.x & 31) == 0) mark_span(g, x.unit, x, worker);
-    attend<DTYPE, D, NT, WARPS>(g, x, split, (x.unit + worker) * g.own.rows,
-                                smem_u32(smem) + warp * C::WARP_BYTES);
+  Begun goes_on = {0, 0, 0, 0, 0, 0};
+  if (lo < hi) {
+    OwnWalk<Steps4<NH>> walk;
+    walk.begin(g, scan, lo, hi);
+    Stretch x;
+    while (walk.next(g, &x)) {
+      float *part = x.s0 > 0 ? part_at<D>(g, worker, kHead)
+                    : x.s1 < x.n ? part_at<D>(g, worker, kTail) : nullptr;
+      attend<DTYPE, D, NT, NH, WARPS>(g, x, split, part, smem + warp * C::WARP_BYTES);
+      if (x.s0 == 0 && x.s1 < x.n)  // the worker's last: steps that follow, a piece each worker
+        goes_on = {1 + static_cast<int>(quotient(x.n - x.s1 + piece - 1, piece)), x.head, x.tok0,
+                   x.ntok, x.lim0, x.kv_len};
+    }
+  }
+  if (lane == 0) begun[worker] = goes_on;
+  if (own.drop) return;
+  bool p = false, q = false;
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Seq s = read_seq<Steps4<NH>>(g, b, &p, &q);
+    if (s.steps == 0)
+      for (int i = 0; i < s.nq; ++i) clear_token<D>(a, s.q0 + i);
+  }
+  if (a.q_offsets) {
+    const int before = a.q_offsets[0], after = a.q_offsets[a.B];
+    for (int t = blockIdx.x; t < before; t += gridDim.x) clear_token<D>(a, t);
+    for (int t = after + blockIdx.x; t < a.T; t += gridDim.x) clear_token<D>(a, t);
   }
 }
 
-// The plan: query rows of a unit, and the scratch.
-struct Plan4 {
-  int split, blocks8, warps;  // blocks of 8 rows in a unit
-  int64_t units;
-  size_t span, lse, o, bytes;
-};
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+// The units that several workers had: blockIdx.x is the worker that began one, a warp
+// takes a row.
+template <int DTYPE, int D>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs g, const Begun *begun) {
+  pdl_begin();
+  constexpr int E = D / 32, kBatch = 8;
+  const int worker = blockIdx.x, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Begun u = begun[worker];
+  if (u.parts == 0 || r >= u.ntok * g.G) return;
+  auto part = [&](int i) { return part_at<D>(g, worker + i, i == 0 ? kTail : kHead); };
+  float x[kBatch][E], o[E], l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  auto fetch = [&](int k) {
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c)
+      if (k + c < u.parts) {
+        const float *src = part(k + c) + r * D + lane * E;
+        if constexpr (E == 4)
+          *reinterpret_cast<float4 *>(x[c]) = *reinterpret_cast<const float4 *>(src);
+        else
+          *reinterpret_cast<float2 *>(x[c]) = *reinterpret_cast<const float2 *>(src);
+      }
+  };
+  float mine = lane < u.parts ? part(lane)[g.own.rows * D + r] : -INFINITY;
+  fetch(0);  // before the maximum is known
+  float top = mine;
+  for (int i = lane + 32; i < u.parts; i += 32) top = fmaxf(top, part(i)[g.own.rows * D + r]);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll 1
+  for (int k = 0; k < u.parts; k += kBatch) {
+    if (k && (k & 31) == 0)
+      mine = k + lane < u.parts ? part(k + lane)[g.own.rows * D + r] : -INFINITY;
+    const float weight = ex2(mine - ref);
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c) {
+      const float w = __shfl_sync(0xffffffffu, weight, (k + c) & 31);
+      l += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = w == 0.0f ? o[e] : fmaf(w, x[c][e], o[e]);
+    }
+    if (k + kBatch < u.parts) fetch(k + kBatch);
+  }
+  const int i = r * g.tpt >> 16;
+  const Row4 row = row_at<D>(g.a, u.tok0 + i, u.head * g.G + r - i * g.G);
+  const float inv = l != 0.0f ? 1.0f / l : min(u.kv_len, u.lim0 + i) > 0 ? NAN : 0.0f;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2 *>(row.o + 4 * lane) =
+        make_uint2(pack2<DTYPE>(o[0] * inv, o[1] * inv), pack2<DTYPE>(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<uint32_t *>(row.o + 2 * lane) = pack2<DTYPE>(o[0] * inv, o[1] * inv);
+  if (row.lse && lane == 0)
+    *row.lse = l != 0.0f ? (ref + log2f(l)) * 0.6931471805599453f : isnan(inv) ? inv : -INFINITY;
+}
 
-Plan4 plan(AttnArgs &g, int T, int B, int max_q, int hq, int hkv, int D) {
-  const int most_rows = D == 128 ? 16 : 32;
+// The plan: query rows of a unit.
+struct Plan4 {
+  int split, blocks8;  // parts of a key head's queries, blocks of 8 rows in a unit
+};
+constexpr int kMostRows4 = 16;  // of a unit
+Plan4 plan(AttnArgs &g, int T, int max_q, int hq, int hkv) {
   const int G = hq / hkv, nq = std::max(1, std::min(max_q, T));
   Plan4 p = {};
   // more query heads than a unit has rows: equal parts of them
-  int Gs = std::min(G, most_rows);
+  int Gs = std::min(G, kMostRows4);
   while (G % Gs != 0) --Gs;
   p.split = G / Gs;
-  const int64_t rows = static_cast<int64_t>(nq) * Gs;
-  p.blocks8 = rows <= 8 ? 1 : rows <= 16 || D == 128 ? 2 : 4;
-  p.warps = p.blocks8 == 1 ? 16 : 8;
+  p.blocks8 = static_cast<int64_t>(nq) * Gs <= 8 ? 1 : 2;
   g.G = Gs;
-  g.own.tok = static_cast<int>(std::min<int64_t>(std::max(1, 8 * p.blocks8 / Gs), nq));
+  g.tpt = (65536 + Gs - 1) / Gs;  // r * tpt >> 16 = r / Gs
+  g.own.tok = std::min(std::max(1, 8 * p.blocks8 / Gs), nq);
   g.own.rows = g.own.tok * Gs;
-  g.own_rows_kernel = B > 0;
-  g.r_on = g.own_rows_kernel;
-  g.r_most = kMaxCtas * kMostWarps4;
-  // blocks of all sequences: the tokens may lie in any of them, max_q in each
-  const int64_t blocks = std::min<int64_t>(
-      B + T / g.own.tok, static_cast<int64_t>(B) * ((nq + g.own.tok - 1) / g.own.tok));
-  p.units = blocks * (hq / Gs);
-  const size_t parts = (static_cast<size_t>(p.units) + kMaxCtas * kMostWarps4) * g.own.rows;
-  p.span = up256(sizeof(SeqMeta) * static_cast<size_t>(B));
-  p.lse = up256(p.span + sizeof(int2) * static_cast<size_t>(p.units));
-  p.o = up256(p.lse + 4 * parts);
-  p.bytes = up256(p.o + 4 * parts * D);
   return p;
 }
+constexpr size_t kBegunBytes = (sizeof(Begun) * kMaxCtas * kMostWarps4 + 255) / 256 * 256;
 
-template <int DTYPE, int D, int NT, int WARPS>
-cudaError_t run(const AttnArgs &g, int split, int ctas, cudaStream_t s) {
-  using C = Cfg4<D, WARPS>;
-  auto kernel = kv4_attention_kernel<DTYPE, D, NT, WARPS>;
+template <int DTYPE, int D, int NT, int NH, int WARPS>
+cudaError_t run(const AttnArgs &g, int split, Begun *begun, int ctas, cudaStream_t s) {
+  using C = Cfg4<D, NH, WARPS>;
+  static_assert(WARPS <= kMostWarps4, "slots of partial results");
+  auto kernel = kv4_attention_kernel<DTYPE, D, NT, NH, WARPS>;
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (err != cudaSuccess) return err;
-  MOE_LAUNCH_PDL(kernel, ctas, WARPS * 32, C::SMEM_BYTES, s, g, split);
+  MOE_LAUNCH_PDL(kernel, ctas, WARPS * 32, C::SMEM_BYTES, s, g, split, begun);
+  MOE_LAUNCH_PDL(kv4_join_kernel<DTYPE, D>, dim3(ctas * WARPS, (g.own.rows + 7) / 8), 256, 0, s, g,
+                 begun);
   return cudaGetLastError();
 }
 template <int DTYPE, int D>
-cudaError_t run_d(const AttnArgs &g, const Plan4 &p, int ctas, cudaStream_t s) {
-  if (p.blocks8 == 1) return run<DTYPE, D, 1, W1>(g, p.split, ctas, s);
-  if constexpr (D == 64)
-    if (p.blocks8 == 4) return run<DTYPE, D, 4, 8>(g, p.split, ctas, s);
-  return run<DTYPE, D, 2, W2>(g, p.split, ctas, s);
+cudaError_t run_d(const AttnArgs &g, const Plan4 &p, Begun *begun, int ctas, cudaStream_t s) {
+  if (p.blocks8 == 1) return run<DTYPE, D, 1, 4, 12>(g, p.split, begun, ctas, s);
+  return run<DTYPE, D, 2, 2, D == 128 ? 8 : 12>(g, p.split, begun, ctas, s);
 }
 
 }  // namespace
 
-size_t kv4_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D, bool smaller) {
+size_t kv4_attention_scratch_bytes(int T, int max_q, int hq, int hkv, int D) {
   AttnArgs g = {};
-  size_t bytes = plan(g, T, B, max_q, hq, hkv, D).bytes;
-  // What no smaller call passes: up to a unit's most rows a smaller max_q can have
-  // more units, past them none.
-  for (int q = std::min(max_q - 1, 32); smaller && q > 0; --q)
-    bytes = std::max(bytes, plan(g, T, B, q, hq, hkv, D).bytes);
-  return bytes;
+  plan(g, T, max_q, hq, hkv);
+  return kBegunBytes +
+         sizeof(float) * kMaxCtas * kMostWarps4 * 2 * static_cast<size_t>(part_floats(g.own.rows, D));
 }
 
 cudaError_t launch_kv4_attention(const PrefixAttnArgs &a, int dtype, cudaStream_t s) {
@@ -608,23 +764,15 @@ cudaError_t launch_kv4_attention(const PrefixAttnArgs &a, int dtype, cudaStream_
   AttnArgs g = {};
   g.a = a;
   const int ctas = std::min(num_sms(), kMaxCtas);
-  const Plan4 p = plan(g, a.T, a.B, a.max_q, a.hq, a.hkv, a.D);
+  const Plan4 p = plan(g, a.T, a.max_q, a.hq, a.hkv);
   g.a.hkv = a.hkv * p.split;  // units are counted by parts of a key head's queries
-  g.meta = reinterpret_cast<SeqMeta *>(a.scratch);
-  g.span = reinterpret_cast<int2 *>(a.scratch + p.span);
-  g.part_lse = reinterpret_cast<float *>(a.scratch + p.lse);
-  g.part_o = reinterpret_cast<float *>(a.scratch + p.o);
-  if (g.r_on) {
-    cudaError_t err;
-    if (dtype == MOE_DTYPE_BF16)
-      err = a.D == 64 ? run_d<MOE_DTYPE_BF16, 64>(g, p, ctas, s)
-                      : run_d<MOE_DTYPE_BF16, 128>(g, p, ctas, s);
-    else
-      err = a.D == 64 ? run_d<MOE_DTYPE_FP16, 64>(g, p, ctas, s)
-                      : run_d<MOE_DTYPE_FP16, 128>(g, p, ctas, s);
-    if (err != cudaSuccess) return err;
-  }
-  return launch_attention_join(g, dtype, ctas, s);
+  Begun *begun = reinterpret_cast<Begun *>(a.scratch);
+  g.part_o = reinterpret_cast<float *>(a.scratch + kBegunBytes);
+  if (dtype == MOE_DTYPE_BF16)
+    return a.D == 64 ? run_d<MOE_DTYPE_BF16, 64>(g, p, begun, ctas, s)
+                     : run_d<MOE_DTYPE_BF16, 128>(g, p, begun, ctas, s);
+  return a.D == 64 ? run_d<MOE_DTYPE_FP16, 64>(g, p, begun, ctas, s)
+                   : run_d<MOE_DTYPE_FP16, 128>(g, p, begun, ctas, s);
 }
 
 }  // namespace moe

@@ -42,7 +42,7 @@ __device__ __forceinline__ int half_row(const AttnArgs &g, int in, int rows) {
 // The workers of a unit, inside the slots whatever stands there (a tiles
 // kernel whose wait ran out leaves spans unwritten).
 __device__ __forceinline__ int2 span_of(const AttnArgs &g, int64_t place, bool rows_kernel) {
-  const int most = rows_kernel ? g.r_most : kMaxCtas;
+  const int most = rows_kernel ? kMaxCtas * kRowWarps : kMaxCtas;
   int2 w = g.span[place];
   w.x = min(max(w.x, 0), most - 1);
   w.y = min(max(w.y, w.x), most - 1);
@@ -286,7 +286,6 @@ Need plan(AttnArgs &g, int T, int B, int max_q, int hq, int hkv, int D, int pref
   g.own_rows_kernel = own && own_by_rows(D, static_cast<int64_t>(nq) * G);
   g.own_on = own && !g.own_rows_kernel;
   g.r_on = g.r_prefix || g.own_rows_kernel;
-  g.r_most = kMaxCtas * kRowWarps;
   g.t_on = g.p_on || g.own_on;
   g.share = g.p_on && g.own_rows_kernel;
   // rows kernel: one 16-row block if all units fit, else 32-row units
@@ -373,14 +372,6 @@ cudaError_t join(const AttnArgs &g, int ctas, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attention_join(const AttnArgs &g, int dtype, int ctas, cudaStream_t s) {
-  if (dtype == MOE_DTYPE_BF16)
-    return g.a.D == 64 ? join<MOE_DTYPE_BF16, 64>(g, ctas, s)
-                       : join<MOE_DTYPE_BF16, 128>(g, ctas, s);
-  return g.a.D == 64 ? join<MOE_DTYPE_FP16, 64>(g, ctas, s)
-                     : join<MOE_DTYPE_FP16, 128>(g, ctas, s);
-}
-
 size_t prefix_attention_scratch_bytes(int T, int B, int max_q, int hq, int hkv, int D,
                                       int prefix_len) {
   // What no smaller call passes.  Either kernel's need grows with every argument,
@@ -420,7 +411,9 @@ cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, int dtype, cudaStre
     const cudaError_t err = launch_attention_rows(g, dtype, ctas, s);
     if (err != cudaSuccess) return err;
   }
-  return launch_attention_join(g, dtype, ctas, s);
+  if (dtype == MOE_DTYPE_BF16)
+    return a.D == 64 ? join<MOE_DTYPE_BF16, 64>(g, ctas, s) : join<MOE_DTYPE_BF16, 128>(g, ctas, s);
+  return a.D == 64 ? join<MOE_DTYPE_FP16, 64>(g, ctas, s) : join<MOE_DTYPE_FP16, 128>(g, ctas, s);
 }
 
 }  // namespace moe
