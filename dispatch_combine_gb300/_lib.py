@@ -971,8 +971,15 @@ def moe_prefix_attention(kv: MoeKv, q, k_cache, v_cache, prefix_pages, prefix_le
 # serving from a cache held in 4 bits, and drafted tokens
 # --------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=None)
+def _one_device():
+    return torch.cuda.device_count() < 2
+
+
 def _here(*tensors):
     """The tensors of a call are on the current device, whose stream it runs on."""
+    if _one_device():
+        return
     for t in tensors:
         if t is not None and t.is_cuda and t.get_device() != _current_device():
             raise ValueError(f"tensor on cuda:{t.get_device()}, not on the current device")
@@ -988,7 +995,7 @@ def moe_kv4_page_bytes(kv: MoeKv) -> int:
 
 
 def _kv4_cache(kv):
-    return kv.num_pages, kv.num_kv_heads, kv.page_size * (kv.head_dim // 2 + kv.head_dim // 16)
+    return kv.num_pages, kv.num_kv_heads, kv.page_size * kv.head_dim * 9 // 16
 
 
 def moe_kv4_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_cache,

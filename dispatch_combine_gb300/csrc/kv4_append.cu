@@ -164,8 +164,10 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const KvAppendArgs a
     const int64_t at = static_cast<int64_t>(blockIdx.x) * TOKENS + tok;
     if (at < a.T) {
       float sn, cs;
-      sine_cosine(turns64(a.inv_freq[k]) * static_cast<uint64_t>(static_cast<int64_t>(a.positions[at])),
-                  &sn, &cs);
+      const float freq = a.inv_freq[k];
+      sine_cosine(turns64(freq) * static_cast<uint64_t>(static_cast<int64_t>(a.positions[at])), &sn,
+                  &cs);
+      if (!isfinite(freq)) sn = cs = NAN;
       s_cos[tok][angle_at(k)] = cs;
       s_sin[tok][angle_at(k)] = sn;
     }

@@ -36,6 +36,7 @@
 // against 64 bits 1.6 times that of the output's rounding with two, 37 sequences of
 // up to 6 tokens and 4099 rows).
 #include <algorithm>
+#include <atomic>
 
 #include "attention.cuh"
 #include "kv4.cuh"
@@ -736,9 +737,17 @@ cudaError_t run(const AttnArgs &g, int split, Begun *begun, int ctas, cudaStream
   using C = Cfg4<D, NH, WARPS>;
   static_assert(WARPS <= kMostWarps4, "slots of partial results");
   auto kernel = kv4_attention_kernel<DTYPE, D, NT, NH, WARPS>;
-  const cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  // once for a device (0.7 us a call)
+  static std::atomic<uint64_t> known{0};
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
   if (err != cudaSuccess) return err;
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if ((known.load(std::memory_order_relaxed) & bit) == 0) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (err != cudaSuccess) return err;
+    known.fetch_or(bit, std::memory_order_relaxed);
+  }
   MOE_LAUNCH_PDL(kernel, ctas, WARPS * 32, C::SMEM_BYTES, s, g, split, begun);
   MOE_LAUNCH_PDL(kv4_join_kernel<DTYPE, D>, dim3(ctas * WARPS, (g.own.rows + 7) / 8), 256, 0, s, g,
                  begun);

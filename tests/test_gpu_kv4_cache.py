@@ -251,3 +251,85 @@ def test_cache_past_32_bit_offsets():
     moe.moe_kv4_append(kv, None, k, v, None, slots, None, kc, vc)
     k2, v2 = moe.moe_kv4_read(kv, slots, kc, vc)
     assert torch.equal(k2, held(k)[0].to(BF16)) and torch.equal(v2, held(v)[0].to(BF16))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("style", [moe.MOE_ROPE_HALF, moe.MOE_ROPE_PAIRS])
+def test_far_and_negative_positions(D, style):
+    """Queries, whose rotation shows the angles: up to 2^31 positions the angle is good to 1.5 * 2^-53 of
+    its turns (the frequency in 53 bits), 2e-7 of a turn at a frequency of 1, and at 10^6 to 3e-11."""
+    pos = i32(0, 1, 999983, -999983, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 7, 12345678)
+    kv = moe.kv_struct(2, 2, D, 16, 1, FP16)
+    q, k = rand(8, 2, D, dtype=FP16, seed=1), rand(8, 2, D, dtype=FP16, seed=2)
+    kc, vc = caches(kv)
+    freq = freqs(D)
+    freq[3] = -freq[3]
+    out = moe.moe_kv4_append(kv, q, k, k, pos, torch.arange(8, device="cuda", dtype=torch.int32), freq, kc, vc, style=style)
+    want, size = turned(q, pos, freq, style)
+    turns = (pos.double().abs()[:, None] * freq.double().abs().max() / 6.283185307179586)[..., None]
+    e = 4 * 2.0 ** -24 + 2 * 6.3 * 1.5 * 2.0 ** -53 * turns       # both sides' angles
+    t = torch.finfo(FP16)
+    assert ((out.double() - want).abs() <= t.eps / 2 * (want.abs() + e * size) + e * size + t.tiny * t.eps / 2).all()
+
+
+def test_many_tokens_take_two_warps_each():
+    """Past eight tokens an SM the kernel has several in a CTA: the last of them short."""
+    T, hq, hkv, D, page = 2051, 6, 2, 128, 64
+    kv = moe.kv_struct(hq, hkv, D, page, -(-T // page), BF16)
+    q, k, v = (rand(T, h, D, seed=s) for h, s in ((hq, 1), (hkv, 2), (hkv, 3)))
+    pos = torch.arange(T, device="cuda", dtype=torch.int32) + 5000
+    slots = torch.randperm(kv.num_pages * page, generator=torch.Generator().manual_seed(1))[:T].to("cuda", torch.int32)
+    slots[7] = -1
+    many, few = caches(kv), caches(kv)
+    a = moe.moe_kv4_append(kv, q, k, v, pos, slots, freqs(D), *many)
+    b = torch.empty_like(a)
+    for t in range(0, T, 200):      # the same tokens in calls of fewer
+        s = slice(t, min(T, t + 200))
+        moe.moe_kv4_append(kv, q[s], k[s], v[s], pos[s], slots[s], freqs(D), *few, q_out=b[s])
+    assert torch.equal(a, b) and torch.equal(many[0], few[0]) and torch.equal(many[1], few[1])
+    rows = [moe.moe_kv4_read(kv, slots, *many) for _ in range(2)]
+    assert torch.equal(rows[0][0], rows[1][0]) and torch.equal(rows[0][1], held(v)[0].to(BF16) * (slots >= 0)[:, None, None])
+
+
+def test_a_frequency_that_is_not_finite():
+    kv = moe.kv_struct(1, 1, 64, 16, 1, BF16)
+    freq = freqs(64)
+    freq[5] = float("inf")
+    freq[9] = float("nan")
+    kc, vc = caches(kv)
+    q = rand(1, 1, 64, seed=1)
+    out = moe.moe_kv4_append(kv, q, q, q, i32(3), i32(0), freq, kc, vc)
+    bad = torch.zeros(64, dtype=torch.bool, device="cuda")
+    bad[[5, 9, 37, 41]] = True
+    assert out[0, 0][bad].isnan().all() and not out[0, 0][~bad].isnan().any()
+    k2, _ = moe.moe_kv4_read(kv, i32(0), kc, vc)
+    assert k2.isnan().all()         # both groups hold one
+
+
+def test_capture_and_replay():
+    """The calls of a step in one graph, slots and positions changing between replays."""
+    kv = moe.kv_struct(4, 2, 64, 16, 4, FP16)
+    q, k, v = (rand(5, h, 64, dtype=FP16, seed=s) for h, s in ((4, 1), (2, 2), (2, 3)))
+    pos, slots = i32(1, 2, 3, 4, 5), i32(0, 1, 2, 3, 4)
+    kc, vc = caches(kv)
+    qo, ko, vo = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+
+    def step():
+        moe.moe_kv4_append(kv, q, k, v, pos, slots, freqs_, kc, vc, q_out=qo)
+        moe.moe_kv4_read(kv, slots, kc, vc, k_out=ko, v_out=vo)
+
+    freqs_ = freqs(64)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(3):
+        slots.copy_(torch.tensor([63, 5 + i, 17, 33, 50], dtype=torch.int32))
+        pos.copy_(torch.arange(5) * (i + 7))
+        graph.replay()
+        got = qo.clone(), ko.clone(), vo.clone()
+        kc2, vc2 = caches(kv)
+        a = moe.moe_kv4_append(kv, q, k, v, pos, slots, freqs_, kc2, vc2)
+        b = moe.moe_kv4_read(kv, slots, kc2, vc2)
+        assert torch.equal(got[0], a) and torch.equal(got[1], b[0]) and torch.equal(got[2], b[1])

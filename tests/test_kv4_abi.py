@@ -181,6 +181,7 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         def get_device(self):
             return 1
 
+    monkeypatch.setattr(_lib, "_one_device", lambda: False)
     monkeypatch.setattr(_lib, "_current_device", lambda: 0)
     with pytest.raises(ValueError):
         _lib._here(None, torch.zeros(1), Elsewhere())
