@@ -325,3 +325,40 @@ def test_cache_past_32_bit_offsets():
     want = small.run()
     got = moe.moe_kv4_attention(kv, small.q, kc, vc, mine[None], small.kv_lens, small.ws, want_lse=True)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_tokens_of_no_sequence():
+    """A batch padded in front and behind: its tokens without a sequence see nothing."""
+    b = Batch([40, 0, 70], [2, 1, 1], 8, 2, 64, 16, seed=1)
+    want = b.run()
+    q = torch.full((9, 8, 64), 3.0, dtype=BF16, device="cuda")
+    q[2:6] = b.q
+    off = torch.tensor([2, 4, 5, 6], dtype=torch.int32, device="cuda")
+    ws = moe.Workspace(moe.moe_kv4_attention_workspace_size(b.kv, 9, 3, 2))
+    out, lse = torch.full_like(q, 7.0), torch.full((9, 8), 7.0, device="cuda")
+    moe.moe_kv4_attention(b.kv, q, b.kc, b.vc, b.table, b.kv_lens, ws, q_offsets=off, max_q=2, out=out, lse=lse)
+    assert torch.equal(out[2:6], want[0]) and torch.equal(lse[2:6], want[1])
+    rest = [0, 1, 6, 7, 8]
+    assert (out[rest] == 0).all() and (lse[rest] == -math.inf).all()
+    assert moe.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("n,hq,hkv,D", [(1500, 2, 1, 64), (700, 6, 3, 128), (4096, 1, 1, 64)])
+def test_many_short_sequences(n, hq, hkv, D):
+    """Several units of a worker, several sequences of a thread of the scan, and none among them."""
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 80, (n,), generator=g).tolist()
+    qs = torch.randint(0, 3, (n,), generator=g).tolist()
+    b = Batch(lens, qs, hq, hkv, D, 16, BF16, seed=5)
+    o, lse = b.run()
+    rows = set(torch.randint(0, b.T, (40,), generator=g).tolist())
+    b.check(o, lse, rows=rows)
+    # the rest against the same sequences in calls of their own kind: nothing is left out
+    assert not o.isnan().any()
+    seen = torch.tensor([i for m, k in zip(lens, qs) for i in [m - k + j + 1 for j in range(k)]], device="cuda") > 0
+    assert torch.equal(lse > -math.inf, seen[:, None].expand_as(lse))
+
+
+def test_one_head_over_all_workers():
+    b = Batch([70001], [1], 3, 1, 128, 64, BF16, seed=9)
+    b.check(*b.run())
