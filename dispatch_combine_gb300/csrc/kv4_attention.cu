@@ -577,7 +577,8 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
 // Walks the units in [lo, hi) of their line, a whole warp, sequence by sequence from
 // the one where the CTA's scan has lo.  (The walk of attention.cuh looks at 32
 // sequences at a time, which a few units a worker do not pay back: 64 sequences of up
-// to 8192 rows 71.6 us with it, TIME_WALK so.)
+// to 8192 rows 71.6 us with it, 70.4 so; one
+// token over 1000 rows 11.2 and 10.8.)
 template <class K>
 struct Walk4 {
   int64_t lo, hi, start, unit_cost;
@@ -713,14 +714,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 // The units that several workers had: blockIdx.x is the worker that began one, a warp
 // takes a row.
 template <int DTYPE, int D>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs g, const Begun *begun) {
+__global__ void __launch_bounds__(256, 4) kv4_join_kernel(const AttnArgs g, const Begun *begun) {
   pdl_begin();
   constexpr int E = D / 32, kBatch = 8;
   const int worker = blockIdx.x, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
   const Begun u = begun[worker];
   if (u.parts == 0 || r >= u.ntok * g.G) return;
-  auto part = [&](int i) { return part_at<D>(g, worker + i, i == 0 ? kTail : kHead); };
+  // from the worker's tail part to the i-th
+  const int two = 2 * part_floats(g.own.rows, D);
+  auto ahead = [&](int i) { return i == 0 ? 0 : i * two + two / 2; };
+  static_assert(kTail == 0 && kHead == 1, "a worker's head part follows its tail part");
+  const float *parts = part_at<D>(g, worker, kTail) + r * D + lane * E;
+  const float *lses = part_at<D>(g, worker, kTail) + g.own.rows * D + r;
   float x[kBatch][E], o[E], l = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
@@ -728,24 +734,24 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs g, const B
 #pragma unroll
     for (int c = 0; c < kBatch; ++c)
       if (k + c < u.parts) {
-        const float *src = part(k + c) + r * D + lane * E;
+        const float *src = parts + ahead(k + c);
         if constexpr (E == 4)
           *reinterpret_cast<float4 *>(x[c]) = *reinterpret_cast<const float4 *>(src);
         else
           *reinterpret_cast<float2 *>(x[c]) = *reinterpret_cast<const float2 *>(src);
       }
   };
-  float mine = lane < u.parts ? part(lane)[g.own.rows * D + r] : -INFINITY;
+  float mine = lane < u.parts ? lses[ahead(lane)] : -INFINITY;
   fetch(0);  // before the maximum is known
   float top = mine;
-  for (int i = lane + 32; i < u.parts; i += 32) top = fmaxf(top, part(i)[g.own.rows * D + r]);
+  for (int i = lane + 32; i < u.parts; i += 32) top = fmaxf(top, lses[ahead(i)]);
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   const float ref = top == -INFINITY ? 0.0f : top;
 #pragma unroll 1
   for (int k = 0; k < u.parts; k += kBatch) {
     if (k && (k & 31) == 0)
-      mine = k + lane < u.parts ? part(k + lane)[g.own.rows * D + r] : -INFINITY;
+      mine = k + lane < u.parts ? lses[ahead(k + lane)] : -INFINITY;
     const float weight = ex2(mine - ref);
 #pragma unroll
     for (int c = 0; c < kBatch; ++c) {
