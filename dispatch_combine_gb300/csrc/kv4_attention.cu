@@ -37,6 +37,7 @@
 // up to 6 tokens and 4099 rows).
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 
 #include "attention.cuh"
 #include "kv4.cuh"
@@ -412,6 +413,35 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
             if (half * 16 + 8 >= lim) sc[half][nt][2 + c] = -INFINITY;
           }
         }
+      // Values that stand for NaN are nothing to rows that do not see them (0 NaN would
+      // be): their scales go, and the scores of those that do see them are the NaN.
+      uint32_t w[NB];
+      const uint32_t at = ss + C::SCALES + lane % (8 * NH) * (2 * C::SB);
+      lds<NB>(at, w);
+      bool even = false, odd = false;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        even |= (w[b] & 0x7C00u) == 0x7C00u;
+        odd |= (w[b] & 0x7C000000u) == 0x7C000000u;
+      }
+      const unsigned evens = __ballot_sync(0xffffffffu, even), odds = __ballot_sync(0xffffffffu, odd);
+      if (evens | odds) {
+        const uint32_t keep = (even ? 0u : 0xFFFFu) | (odd ? 0u : 0xFFFF0000u);
+        if (lane < 8 * NH)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * b), "r"(w[b] & keep) : "memory");
+        __syncwarp();
+        const unsigned mine = (gr & 1 ? odds : evens) >> (gr >> 1);
+#pragma unroll
+        for (int half = 0; half < NH; ++half)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((mine >> (8 * half + 4 * (e >> 1)) & 1) && sc[half][nt][e] != -INFINITY)
+                sc[half][nt][e] = NAN;
+      }
     }
     // ---- exponents.  The running maximum moves when a score passes it by the lag,
     // and the exponent of the value scales when one passes it (the test is of the
@@ -464,7 +494,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
           // each column by its own scores, so that no head's bits depend on another's
           is[c] = old + (ev - ev1);
           if (s == x.s0 || fmaf(top, u, old) > Prob4::kOff + Prob4::kLag - ev)
-            is[c] = fmaf(-fmaxf(top, -Prob4::kMost / u), u, Prob4::kOff - ev1);
+            is[c] = fmaf(-fmaxf(top, fmaxf(-Prob4::kMost / u, -FLT_MAX)), u, Prob4::kOff - ev1);
           f[c] = ex2(is[c] - old);
           if (s == x.s0) f[c] = 0.0f;
         }

@@ -651,7 +651,8 @@ size_t moe_kv4_page_bytes(const moe_kv_t *kv);
 /*
  * Append T tokens to the 4-bit cache, with the position rotation on the way: the
  * arguments, checks and errors of moe_kv_append.  Keys are quantised as rotated
- * in fp32, without a rounding to 16 bits between.
+ * in fp32, without a rounding to 16 bits between.  Slots must be distinct: two
+ * tokens with one slot may leave codes of one and scales of the other.
  */
 moe_status_t moe_kv4_append(const moe_kv_t *kv, int32_t T, const void *q, int64_t q_stride,
                             const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -686,11 +687,13 @@ moe_status_t moe_kv4_read(const moe_kv_t *kv, int32_t n, const int32_t *slots,
  * moe_prefix_attention.
  *   The cache's numbers and scales enter the products unrounded; queries are
  *   held in fp16 after each row's power of two is taken out (elements below 2^-28
- *   of the row's largest lose bits); the probabilities, and their products with
- *   the value scales, are rounded to fp16.  A head whose query passes 2^115, or
- *   holds a NaN or an infinity, or whose largest score passes 1.1e7 in magnitude,
- *   gets NaN.
- * Rows below kv_lens must not stand for NaN; what lies past kv_lens is never used.
+ *   of the row's largest, or below 2^-36, lose bits); the products of the
+ *   probabilities with the value scales are rounded to fp16, for bf16 the
+ *   probabilities before them too.  A head whose query passes 2^115, or holds a NaN
+ *   or an infinity, or whose largest score passes 1.1e7 in magnitude, gets NaN.
+ * A row that stands for NaN makes NaN of the query heads that see it (at least of
+ * the elements of its group, where only its value does) and is nothing to others;
+ * what lies past kv_lens is never used.
  * A workspace sized for some T, num_seqs and max_q (and heads) serves every call
  * in which none of the three is larger.
  */
@@ -721,7 +724,7 @@ moe_status_t moe_kv4_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, 
  * after them comes from max(target_a - draft_a, 0) (without `draft`: target_a
  * without x) if a < n, or from target_n: the first token at which the running sum
  * passes u * the whole.  out_tokens [T] int32: the a drafts that stand, that
- * token, and -1 behind it.
+ * token, and -1 behind it; entries of no sequence are left as they were.
  * Differences are rounded to fp32, sums are exact (weights count in units of
  * 2^-60; a row's should add up to less than 16).  A weight that is NaN or
  * negative counts as 0, one above 1 as 1.  Where nothing of the difference is

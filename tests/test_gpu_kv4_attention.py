@@ -141,6 +141,9 @@ def test_more_new_tokens_than_rows():
     o, lse = b.run()
     b.check(o, lse)
     assert (o[:3] == 0).all() and (lse[5:8] == -math.inf).all()
+    # and with scores too small to be anything: their mean
+    o, lse = b.run(scale=1e-38)
+    b.check(o, lse, scale=1e-38)
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -219,6 +222,36 @@ def test_keys_that_stand_for_nan():
     o, lse = b.run()
     assert o[0].isnan().all() and lse[0].isnan().all() and not o[1].isnan().any()
     b.check(o, lse, rows={1})
+
+
+@pytest.mark.parametrize("hq,hkv,D,dtype", [(8, 2, 128, BF16), (8, 2, 64, FP16), (28, 4, 64, BF16), (6, 3, 128, FP16)])
+@pytest.mark.parametrize("what", ["k", "v", "both"])
+def test_drafts_that_stand_for_nan(hq, hkv, D, dtype, what):
+    """The rows of drafts that are not seen touch nothing: neither tokens before them nor other heads."""
+    lens, qs = [70, 64, 6, 300, 129], [6, 5, 6, 1, 4]
+    b = Batch(lens, qs, hq, hkv, D, 16, dtype, seed=9)
+    clean, _ = b.run()
+    bad = {0: 67, 1: 63, 2: 1, 4: 127}          # sequence: its row with a NaN in head 1, group 1
+    for seq, r in bad.items():
+        if what != "v":
+            b.k[seq][r, 1, 40] = float("nan")
+        if what != "k":
+            b.v[seq][r, 1, 40] = float("nan")
+        slot = (b.table[seq, r // 16] * 16 + r % 16).to(torch.int32)[None]
+        moe.moe_kv4_append(b.kv, None, b.k[seq][r:r + 1], b.v[seq][r:r + 1], None, slot, None, b.kc, b.vc)
+    o, lse = b.run()
+    G, at, blind = hq // hkv, 0, set()
+    for seq, (n, m) in enumerate(zip(lens, qs)):
+        for i in range(m):
+            if seq in bad and n - m + i >= bad[seq]:
+                hit = o[at + i, G:2 * G]
+                assert hit[:, 32:64].isnan().all()
+                assert torch.equal(o[at + i, :G], clean[at + i, :G]) and torch.equal(o[at + i, 2 * G:], clean[at + i, 2 * G:])
+            else:
+                blind.add(at + i)
+        at += m
+    assert len(blind) == 3 + 4 + 1 + 1 + 2
+    b.check(o, lse, rows=blind)
 
 
 def test_strided_queries_and_outputs():
