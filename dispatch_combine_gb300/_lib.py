@@ -1095,7 +1095,7 @@ def moe_verify_drafts(target, tokens, uniforms, offsets, draft=None, ws: Workspa
     moe.h).  target [T, V] and draft (None: drafts taken without a draw) fp32, bf16
     or fp16, rows dense; tokens [T] int32, uniforms [T] fp32, offsets [B + 1] int32.
     Returns (accepted [B] int32, out_tokens [T] int32: the drafts that stand, the
-    token after them, -1 behind it)."""
+    token after them, -1 behind it; entries of no sequence are not written)."""
     if target.dim() != 2:
         raise ValueError("target: expected [T, V]")
     shape, dt = target.shape, target.dtype

@@ -2,8 +2,15 @@
 // quantisation, paged write) and read back to 16 bits (moe_kv4_read).
 //
 //   k' = R(position) k;  per 32 elements s = rn16(max|k'| / 7), n = rn(k' / s) + 8
-// Both are bound by HBM: a token's queries, keys and values are read once, and
-// what is written of keys and values is 9/32 of it.
+// Both are bound by HBM where there are many rows: a token's queries, keys and values
+// are read once, and what is written of keys and values is 9/32 of it.  16384 tokens
+// of 64 + 8 heads of 128 appended and read back (690 MB) take 119 us, 0.86 of the
+// measured copy bandwidth; 131072 rows of 8 heads of 128 read back into a 16-bit
+// cache (689 MB) 117 us, 0.87.  Few rows cost their launch: 64 tokens appended and
+// read back 5.2 us.
+//   What the append was bound by first was arithmetic: with sines in 64 bits and
+// divisions as they are written (119 us now) it was 216, with either of the two
+// replaced 194.
 #include "kv4.cuh"
 
 namespace moe {
@@ -360,7 +367,9 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
 // what a lane of the attention has of a row, so that codes and scales come in one
 // load each (keys: 8 elements of every group, four lanes a row; values: 4 of every
 // group, eight lanes a row, and the row's half of its pair's words).  The slots of
-// the next rows are on their way while these are read.
+// the next rows are on their way while these are read.  131072 rows of 8 heads of
+// 128: 117 us; 182 with a thread for every 8 elements and one load for each of their
+// parts, 137 with 16 rows a warp (spills), 174 with 6 CTAs an SM.
 constexpr int kReadRows = 8, kReadWarps = 8, kReadCtas = 4;  // CTAs of an SM
 template <int DTYPE, int D, bool IS_K>
 __device__ __forceinline__ void read_head(const Kv4ReadArgs &a, int h, int64_t block, int64_t step) {
@@ -455,11 +464,18 @@ __global__ void __launch_bounds__(kReadWarps * 32, kReadCtas) kv4_read_kernel(co
 
 template <int DTYPE, int D>
 cudaError_t append(const KvAppendArgs &a, cudaStream_t s) {
-  // two warps a token where that still gives every SM several CTAs
-  if (a.T >= 8 * num_sms())
-    MOE_LAUNCH_PDL(kv4_append_kernel<DTYPE, D, 2>, (static_cast<unsigned>(a.T) + 3) / 4, 256, 0, s, a);
+  // Warps of a token: eight while the CTAs are one wave, then fewer, whose units in
+  // flight are more.  us with 8, 4, 2 of them, 64 + 8 heads of 128 and the rows read
+  // back: 304 tokens 6.0, 6.4, 8.4; 608 8.3, 8.0, 9.5; 1216 16.0, 14.7, 15.0; 2432
+  // 26.2, 23.9, 24.3; 16384 141, 122, 119.  28 + 4 heads of 64: 152 tokens 4.5, 4.8,
+  // 5.1; 608 5.7, 5.4, 5.4; 4096 24.0, 18.4, 15.0.
+  const unsigned T = static_cast<unsigned>(a.T);
+  if (a.T < 4 * num_sms())
+    MOE_LAUNCH_PDL(kv4_append_kernel<DTYPE, D, 8>, T, 256, 0, s, a);
+  else if (a.T < 12 * num_sms())
+    MOE_LAUNCH_PDL(kv4_append_kernel<DTYPE, D, 4>, (T + 1) / 2, 256, 0, s, a);
   else
-    MOE_LAUNCH_PDL(kv4_append_kernel<DTYPE, D, 8>, static_cast<unsigned>(a.T), 256, 0, s, a);
+    MOE_LAUNCH_PDL(kv4_append_kernel<DTYPE, D, 2>, (T + 3) / 4, 256, 0, s, a);
   return cudaGetLastError();
 }
 template <int DTYPE, int D>

@@ -4,7 +4,11 @@
 //   draft x of row i stands iff u_i q_i(x) < p_i(x) and all before it stand;
 //   the first that falls leaves the token to max(p_i - q_i, 0), none to p_n:
 //   token = min { v : sum_{w <= v} r_w > u sum r }.
-// One row of p and one of q are read for each sequence, by a cluster of CTAs.
+// One row of p and one of q are read for each sequence, by a cluster of CTAs: 64
+// sequences of 7 drafts over 131072 tokens in fp32 (67 MB) take 16 us, 0.62 of the
+// measured copy bandwidth; one sequence over 32000 5.1.  What bounds it is the chain
+// of dependent reads: offsets, drafts, their probabilities, the row, the sums of the
+// cluster's CTAs, and the border's piece once more (from L2).
 //
 // The sums are whole numbers: a weight in [0, 1] counts in units of 2^-60, so
 // they are exact in any order (to 2^-60 a weight), and which token is the first
@@ -16,7 +20,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kSlots = 2;  // of a lane on their way while as many are summed
+constexpr int kSlots = 2;  // of a lane on their way while as many are summed (23.1 us; 1: 23.5, 3: 26.4)
 
 template <int DTYPE>
 __device__ __forceinline__ float prob_at(const void *p, int64_t i) {
@@ -365,7 +369,15 @@ cudaError_t run(const VerifyArgs &a, int ctas, cudaStream_t s) {
 
 cudaError_t launch_verify(const VerifyArgs &a, int dtype, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
-  const int ctas = 8;  // a warp looks at 64 parts
+  // CTAs of a sequence, 8 at most (a warp looks at 64 parts): fewer where there are
+  // more sequences than one wave has room for, or not a slot for every thread.  us with
+  // 8, 4, 2, 1 of them, fp32: 64 sequences of 131072 tokens 16.0, 20.1, 32.6, 58.6; 512
+  // of 32000 50.6, 35.4, 29.4, 28.2; 1024 of 8192 81, 43, 29, 21; 64 of 1000 7.2,
+  // 5.6, 4.9, 4.9; one of 32000 5.1, 5.7, 7.1, 10.7.
+  const int slots = a.vocab / (dtype == MOE_DTYPE_FP32 ? 4 : 8);
+  int ctas = 8;
+  while (ctas > 1 && (static_cast<int64_t>(a.B) * ctas > 4 * num_sms() || ctas * kThreads > slots))
+    ctas /= 2;
   if (dtype == MOE_DTYPE_FP32) return run<MOE_DTYPE_FP32>(a, ctas, s);
   if (dtype == MOE_DTYPE_BF16) return run<MOE_DTYPE_BF16>(a, ctas, s);
   return run<MOE_DTYPE_FP16>(a, ctas, s);

@@ -112,7 +112,7 @@ def test_rotation(D, rot, style, dtype):
     near = off <= (2.0 ** -10 + t.eps / 2) * ref.abs() + 1e-7
     share = want / scale
     border = ((share.abs() - 0.5) - torch.round(share.abs() - 0.5)).abs()
-    at_border = (border <= 2 * e * spread / scale + 7 * 2.0 ** -10 * 0) & (off <= 1.01 * scale + t.eps / 2 * ref.abs())
+    at_border = (border <= 2 * e * spread / scale) & (off <= 1.01 * scale + t.eps / 2 * ref.abs())
     # a scale that is its neighbour moves the borders by up to 7 * 2^-10 of a code
     groups = lambda x: x.unflatten(-1, (-1, GROUP))  # noqa: E731
     exact = groups(want).abs().amax(-1) / 7
@@ -122,6 +122,23 @@ def test_rotation(D, rot, style, dtype):
     at_moved = unsure & (border <= 7 * 2.0 ** -10) & (off <= 1.01 * scale + t.eps / 2 * ref.abs())
     assert (near | at_border | at_moved).all()
     assert (~near).sum() <= 8       # chances of 1e-6 an element
+
+
+@pytest.mark.parametrize("T", [700, 1300, 2605])
+@pytest.mark.parametrize("D,style,dtype", [(128, moe.MOE_ROPE_HALF, BF16), (64, moe.MOE_ROPE_PAIRS, FP16)])
+def test_a_token_is_the_same_among_many(T, D, style, dtype):
+    """Bits do not depend on how many tokens a call has (and so on the warps that a token gets)."""
+    hq, hkv, page = 6, 3, 64
+    kv = moe.kv_struct(hq, hkv, D, page, -(-T // page), dtype)
+    q, k, v = (rand(T, h, D, dtype=dtype, seed=s) for h, s in ((hq, 1), (hkv, 2), (hkv, 3)))
+    pos = torch.randint(0, 2 ** 31 - 1, (T,), generator=torch.Generator().manual_seed(T)).to("cuda", torch.int32)
+    slots = torch.randperm(T, generator=torch.Generator().manual_seed(1)).to("cuda", torch.int32)
+    kc, vc = caches(kv)
+    out = moe.moe_kv4_append(kv, q, k, v, pos, slots, freqs(D), kc, vc, style=style)
+    few_k, few_v = caches(kv)
+    few = torch.cat([moe.moe_kv4_append(kv, q[i:i + 90], k[i:i + 90], v[i:i + 90], pos[i:i + 90], slots[i:i + 90],
+                                        freqs(D), few_k, few_v, style=style) for i in range(0, T, 90)])
+    assert torch.equal(out, few) and torch.equal(kc, few_k) and torch.equal(vc, few_v)
 
 
 def test_values_near_the_ends():

@@ -111,6 +111,8 @@ def test_many_drafts_and_many_sequences():
     assert acc.max() > 20            # past one warp's drafts
     check(*batch([1 + b % 4 for b in range(300)], 129, 2, FP32))
     check(*batch([1] * 700, 64, 3, BF16, True))
+    for n in (80, 160, 310):         # clusters of 4, 2 and 1 where rows are long enough for more
+        check(*batch([1 + b % 2 for b in range(n)], 9001, n, FP32))
 
 
 def test_rows_with_strides_and_room_behind():
