@@ -21,11 +21,18 @@
 // those.
 //
 // Bound by HBM where contexts are long: 16 sequences of up to 131072 rows (8 key heads
-// of 128, 8 query heads each; 1.30 GB) take 202 us, 0.95 of the measured copy
-// bandwidth; without the arithmetic 198.  64 of up to 8192 (364 MB) take 71: 12 us are
-// the two launches, the first rows' way and the join.  Several queries of a sequence
-// are bound by the arithmetic (540 instructions for 32 keys x 8 rows of 128): 37
-// sequences of up to 4099, 6 tokens of 7 heads of 64 each (20 MB) 29 us.
+// of 128, 8 query heads each; 1.30 GB) take 200 us, 0.96 of the measured copy
+// bandwidth; without the arithmetic 198.  64 of up to 8192 (364 MB) take 71, 17 of them
+// outside the stream: the two launches and the scan 5, pages and first rows 3, the
+// last rows' way and the join.  Several queries of a sequence are bound by the
+// arithmetic (510 instructions for 32 keys x 8 rows of 128): 37 sequences of up to
+// 4099, 6 tokens of 7 heads of 64 each (20 MB) 28.5 us.
+//   Other ways, each measured against this one as it then was (64 sequences, or 16
+// where it says so): the offset of the values by one more product instead of a
+// subtraction 81 -> 85 us; 16 warps (128 registers, spills) 73 -> 83, 10 or 11 warps
+// 75 to 79; the scores of the next step ahead of this one's softmax 212 -> 225 (16
+// sequences); bulk copies issued by single lanes 217 -> 237 (16); neighbouring pieces
+// on one SM, joined in shared memory 72 -> 84.
 //
 // Rounded to fewer bits: queries to fp16 after taking out each row's power of two
 // (its largest element is put at 2^14: bf16 ones lose nothing above 2^-28 of it);
