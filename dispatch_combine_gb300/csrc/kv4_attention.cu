@@ -17,8 +17,8 @@
 // that is cut into a piece for each warp (attention.cuh): every warp is a worker on
 // its own and streams steps of keys through a private ring in shared memory
 // (cp.async).  A unit that one warp has whole leaves as it should be; of others every
-// warp keeps its part (normalised, with its log-sum-exp), and kv4_join_kernel joins
-// those.
+// warp keeps its part (normalised, with its log-sum-exp), and the joins
+// put those together.
 //
 // Bound by HBM where contexts are long: 16 sequences of up to 131072 rows (8 key heads
 // of 128, 8 query heads each; 1.30 GB) take 200 us, 0.96 of the measured copy
@@ -26,7 +26,7 @@
 // outside the stream: the two launches and the scan 5, pages and first rows 3, the
 // last rows' way and the join.  Several queries of a sequence are bound by the
 // arithmetic (510 instructions for 32 keys x 8 rows of 128): 37 sequences of up to
-// 4099, 6 tokens of 7 heads of 64 each (20 MB) 28.5 us.
+// 4099, 6 tokens of 7 heads of 64 each (20 MB) 25 us.
 //   Other ways, each measured against this one as it then was (64 sequences, or 16
 // where it says so): the offset of the values by one more product instead of a
 // subtraction 81 -> 85 us; 16 warps (128 registers, spills) 73 -> 83, 10 or 11 warps
@@ -54,11 +54,12 @@ namespace {
 
 // A step is NH runs of 16 keys.  What is done once a step (the copies' addresses,
 // the test for the maximum) is a third of the instructions at 32 keys, and longer
-// straight code fills the waits of the three warps that a scheduler has: 16
-// sequences of up to 131072 rows took 215 us with 32 keys, 202 with 64; two blocks of
-// query rows leave no registers for it (37 sequences, 6 tokens of 7 heads of 64: 29.3
-// and 30.2 us).  A unit costs its start besides: 64 sequences of 8192 rows, 16 query
-// heads each: 112 us counting 2 steps of 32 for it, 105 counting 4.
+// straight code fills the waits of the two or three warps that a scheduler has: 16
+// sequences of up to 131072 rows took 215 us with 32 keys, 202 with 64; 37 sequences,
+// 6 tokens of 7 heads of 64: 28.7 with 32 keys and 12 warps, 28.4 with 64 and 12, 25.2
+// with 64 and 8 (fewer parts to join).  Two blocks of query rows of 128 leave no
+// registers for 64.  A unit costs its start besides: 64 sequences of 8192 rows, 16
+// query heads each: 112 us counting 2 steps of 32 for it, 105 counting 4.
 template <int NH>
 struct Steps4 {
   static constexpr int kKeys = 16 * NH, kUnitCost = NH == 4 ? 2 : 4;
@@ -682,6 +683,11 @@ __device__ __forceinline__ void clear_token(const PrefixAttnArgs &a, int64_t t) 
 struct Begun {
   int parts, head, tok0, ntok, lim0, kv_len;
 };
+// A short form of it where there are at most kFewUnits: the unit's number and its parts.
+constexpr int kFewUnits = 64;
+__device__ __forceinline__ int short_form(const PrefixAttnArgs &a, const Begun &u) {
+  return u.parts * kFewUnits + (u.tok0 * a.hkv + u.head) % kFewUnits;
+}
 // A worker has at most two parts: of a unit begun before it, of one that goes on after.
 enum { kTail = 0, kHead = 1 };
 __host__ __device__ constexpr int part_floats(int rows, int D) {  // 16-byte aligned rows
@@ -694,7 +700,7 @@ __device__ __forceinline__ float *part_at(const AttnArgs &g, int worker, int whi
 
 template <int DTYPE, int D, int NT, int NH, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 1)
-    kv4_attention_kernel(const __grid_constant__ AttnArgs g, const int split, Begun *begun) {
+    kv4_attention_kernel(const __grid_constant__ AttnArgs g, const int split, Begun *begun, int *few) {
   using C = Cfg4<D, NH, WARPS>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ ScanShared<WARPS * 32> scan;
@@ -733,7 +739,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
       if (x.s1 < x.n) break;
     }
   }
-  if (lane == 0) begun[worker] = goes_on;
+  if (lane == 0) {
+    begun[worker] = goes_on;
+    if (few) few[worker] = short_form(a, goes_on);
+  }
   if (own.drop) return;
   bool p = false, q = false;
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -748,48 +757,44 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   }
 }
 
-// The units that several workers had: blockIdx.x is the worker that began one, a warp
-// takes a row.
-template <int DTYPE, int D>
-__global__ void __launch_bounds__(256, 4) kv4_join_kernel(const AttnArgs g, const Begun *begun) {
-  pdl_begin();
+// Of a row's parts those of the workers sub, sub + EVERY, ... after the first, by a
+// warp: their sum (rows of D from `parts` on, log2-sum-exps from `lses` on, both the first
+// worker's tail part) as o and l, to the power of two `ref`.
+template <int D, int EVERY>
+__device__ __forceinline__ void add_parts(const float *parts, const float *lses, int two, int n, int sub,
+                                          float (&o)[D / 32], float *sum, float *ref) {
   constexpr int E = D / 32, kBatch = 8;
-  const int worker = blockIdx.x, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const Begun u = begun[worker];
-  if (u.parts == 0 || r >= u.ntok * g.G) return;
-  // from the worker's tail part to the i-th
-  const int two = 2 * part_floats(g.own.rows, D);
-  auto ahead = [&](int i) { return i == 0 ? 0 : i * two + two / 2; };
+  const int lane = threadIdx.x & 31, count = EVERY == 1 ? n : (n - sub + EVERY - 1) / EVERY;
+  auto ahead = [&](int i) {
+    const int k = EVERY == 1 ? i : sub + i * EVERY;
+    return k == 0 ? 0 : k * two + two / 2;
+  };
   static_assert(kTail == 0 && kHead == 1, "a worker's head part follows its tail part");
-  const float *parts = part_at<D>(g, worker, kTail) + r * D + lane * E;
-  const float *lses = part_at<D>(g, worker, kTail) + g.own.rows * D + r;
-  float x[kBatch][E], o[E], l = 0.0f;
+  float x[kBatch][E], l = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
   auto fetch = [&](int k) {
 #pragma unroll
     for (int c = 0; c < kBatch; ++c)
-      if (k + c < u.parts) {
-        const float *src = parts + ahead(k + c);
+      if (k + c < count) {
+        const float *src = parts + ahead(k + c) + lane * E;
         if constexpr (E == 4)
           *reinterpret_cast<float4 *>(x[c]) = *reinterpret_cast<const float4 *>(src);
         else
           *reinterpret_cast<float2 *>(x[c]) = *reinterpret_cast<const float2 *>(src);
       }
   };
-  float mine = lane < u.parts ? lses[ahead(lane)] : -INFINITY;
+  float mine = lane < count ? lses[ahead(lane)] : -INFINITY;
   fetch(0);  // before the maximum is known
   float top = mine;
-  for (int i = lane + 32; i < u.parts; i += 32) top = fmaxf(top, lses[ahead(i)]);
+  for (int i = lane + 32; i < count; i += 32) top = fmaxf(top, lses[ahead(i)]);
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  const float ref = top == -INFINITY ? 0.0f : top;
+  top = top == -INFINITY ? 0.0f : top;
 #pragma unroll 1
-  for (int k = 0; k < u.parts; k += kBatch) {
-    if (k && (k & 31) == 0)
-      mine = k + lane < u.parts ? lses[ahead(k + lane)] : -INFINITY;
-    const float weight = ex2(mine - ref);
+  for (int k = 0; k < count; k += kBatch) {
+    if (k && (k & 31) == 0) mine = k + lane < count ? lses[ahead(k + lane)] : -INFINITY;
+    const float weight = ex2(mine - top);
 #pragma unroll
     for (int c = 0; c < kBatch; ++c) {
       const float w = __shfl_sync(0xffffffffu, weight, (k + c) & 31);
@@ -797,18 +802,100 @@ __global__ void __launch_bounds__(256, 4) kv4_join_kernel(const AttnArgs g, cons
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = w == 0.0f ? o[e] : fmaf(w, x[c][e], o[e]);
     }
-    if (k + kBatch < u.parts) fetch(k + kBatch);
+    if (k + kBatch < count) fetch(k + kBatch);
   }
-  const int i = r * g.tpt >> 16;
+  *sum = l;
+  *ref = top;
+}
+template <int DTYPE, int D>
+__device__ __forceinline__ void write_joined(const AttnArgs &g, const Begun &u, int r,
+                                             const float (&o)[D / 32], float l, float ref) {
+  const int lane = threadIdx.x & 31, i = r * g.tpt >> 16;
   const Row4 row = row_at<D>(g.a, u.tok0 + i, u.head * g.G + r - i * g.G);
   const float inv = l != 0.0f ? 1.0f / l : min(u.kv_len, u.lim0 + i) > 0 ? NAN : 0.0f;
-  if constexpr (E == 4)
+  if constexpr (D == 128)
     *reinterpret_cast<uint2 *>(row.o + 4 * lane) =
         make_uint2(pack2<DTYPE>(o[0] * inv, o[1] * inv), pack2<DTYPE>(o[2] * inv, o[3] * inv));
   else
     *reinterpret_cast<uint32_t *>(row.o + 2 * lane) = pack2<DTYPE>(o[0] * inv, o[1] * inv);
   if (row.lse && lane == 0)
     *row.lse = l != 0.0f ? (ref + log2f(l)) * 0.6931471805599453f : isnan(inv) ? inv : -INFINITY;
+}
+
+// The units that several workers had: blockIdx.x is the worker that began one, a warp
+// takes a row.
+template <int DTYPE, int D>
+__global__ void __launch_bounds__(256, 4) kv4_join_kernel(const AttnArgs g, const Begun *begun) {
+  pdl_begin();
+  const int worker = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Begun u = begun[worker];
+  if (u.parts == 0 || r >= u.ntok * g.G) return;
+  float o[D / 32], l, ref;
+  add_parts<D, 1>(part_at<D>(g, worker, kTail) + r * D, part_at<D>(g, worker, kTail) + g.own.rows * D + r,
+                  2 * part_floats(g.own.rows, D), u.parts, 0, o, &l, &ref);
+  write_joined<DTYPE, D>(g, u, r, o, l, ref);
+}
+
+// The same where a batch has few units, which may have many parts each: blockIdx.x is a
+// unit's number, blockIdx.y its row, whose parts the CTA's warps take in turn.  One token
+// over 1000 rows (16 parts; 8 + 8 x 8 heads of 128) 11.4 us with it, 10.8 without, over
+// 2000 11.6 and 12.0, over 8000 14.6 and 20.8, over 131072 44 and 58.
+template <int DTYPE, int D>
+__global__ void __launch_bounds__(256) kv4_join_few_kernel(const AttnArgs g, const Begun *begun,
+                                                           const int *few, const int workers) {
+  pdl_begin();
+  constexpr int E = D / 32, kWarps = 8;
+  __shared__ __align__(16) float s_o[kWarps][D];
+  __shared__ float s_ref[kWarps], s_l[kWarps];
+  __shared__ int s_worker, s_parts;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
+  bool found = false;
+#pragma unroll
+  for (int k = 0; k < kMaxCtas * kMostWarps4; k += 4 * 256) {
+    const int i = k + 4 * threadIdx.x;
+    if (i >= workers) continue;  // a multiple of 4
+    const int4 w = *reinterpret_cast<const int4 *>(few + i);
+    const int of[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (of[c] >= kFewUnits && of[c] % kFewUnits == static_cast<int>(blockIdx.x)) {
+        found = true;
+        s_worker = i + c;
+        s_parts = of[c] / kFewUnits;
+      }
+  }
+  if (!__syncthreads_or(found)) return;  // no unit, or one that a worker has whole
+  const int worker = s_worker;
+  const Begun u = begun[worker];
+  float o[E], l, ref;
+  add_parts<D, kWarps>(part_at<D>(g, worker, kTail) + r * D,
+                       part_at<D>(g, worker, kTail) + g.own.rows * D + r,
+                       2 * part_floats(g.own.rows, D), s_parts, warp, o, &l, &ref);
+  if (r >= u.ntok * g.G) return;  // the whole CTA
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+  if (lane == 0) {
+    s_ref[warp] = l == 0.0f ? -INFINITY : ref;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  ref = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, s_ref[w]);
+  ref = ref == -INFINITY ? 0.0f : ref;
+  l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 1
+  for (int w = 0; w < kWarps; ++w) {
+    const float weight = ex2(s_ref[w] - ref);
+    if (weight == 0.0f) continue;
+    l = fmaf(weight, s_l[w], l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(weight, s_o[w][lane * E + e], o[e]);
+  }
+  write_joined<DTYPE, D>(g, u, r, o, l, ref);
 }
 
 // The plan: query rows of a unit.
@@ -831,6 +918,7 @@ Plan4 plan(AttnArgs &g, int T, int max_q, int hq, int hkv) {
   return p;
 }
 constexpr size_t kBegunBytes = (sizeof(Begun) * kMaxCtas * kMostWarps4 + 255) / 256 * 256;
+constexpr size_t kFewBytes = (sizeof(int) * kMaxCtas * kMostWarps4 + 255) / 256 * 256;
 
 template <int DTYPE, int D, int NT, int NH, int WARPS>
 cudaError_t run(const AttnArgs &g, int split, Begun *begun, int ctas, cudaStream_t s) {
@@ -848,15 +936,23 @@ cudaError_t run(const AttnArgs &g, int split, Begun *begun, int ctas, cudaStream
     if (err != cudaSuccess) return err;
     known.fetch_or(bit, std::memory_order_relaxed);
   }
-  MOE_LAUNCH_PDL(kernel, ctas, WARPS * 32, C::SMEM_BYTES, s, g, split, begun);
-  MOE_LAUNCH_PDL(kv4_join_kernel<DTYPE, D>, dim3(ctas * WARPS, (g.own.rows + 7) / 8), 256, 0, s, g,
-                 begun);
+  const int64_t units = static_cast<int64_t>(g.a.T) * g.a.hkv;  // at most, and their parts:
+  const int64_t parts = (static_cast<int64_t>(g.a.max_pages) << g.a.page_shift) / C::KEYS;
+  int *few = nullptr;
+  if (units <= kFewUnits && parts > 20) few = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(begun) + kBegunBytes);
+  MOE_LAUNCH_PDL(kernel, ctas, WARPS * 32, C::SMEM_BYTES, s, g, split, begun, few);
+  if (few)
+    MOE_LAUNCH_PDL(kv4_join_few_kernel<DTYPE, D>, dim3(static_cast<unsigned>(units), g.own.rows), 256, 0, s,
+                   g, begun, few, ctas * WARPS);
+  else
+    MOE_LAUNCH_PDL(kv4_join_kernel<DTYPE, D>, dim3(ctas * WARPS, (g.own.rows + 7) / 8), 256, 0, s, g,
+                   begun);
   return cudaGetLastError();
 }
 template <int DTYPE, int D>
 cudaError_t run_d(const AttnArgs &g, const Plan4 &p, Begun *begun, int ctas, cudaStream_t s) {
   if (p.blocks8 == 1) return run<DTYPE, D, 1, 4, 12>(g, p.split, begun, ctas, s);
-  return run<DTYPE, D, 2, 2, D == 128 ? 8 : 12>(g, p.split, begun, ctas, s);
+  return run<DTYPE, D, 2, D == 128 ? 2 : 4, 8>(g, p.split, begun, ctas, s);
 }
 
 }  // namespace
@@ -864,7 +960,7 @@ cudaError_t run_d(const AttnArgs &g, const Plan4 &p, Begun *begun, int ctas, cud
 size_t kv4_attention_scratch_bytes(int T, int max_q, int hq, int hkv, int D) {
   AttnArgs g = {};
   plan(g, T, max_q, hq, hkv);
-  return kBegunBytes +
+  return kBegunBytes + kFewBytes +
          sizeof(float) * kMaxCtas * kMostWarps4 * 2 * static_cast<size_t>(part_floats(g.own.rows, D));
 }
 
@@ -876,7 +972,7 @@ cudaError_t launch_kv4_attention(const PrefixAttnArgs &a, int dtype, cudaStream_
   const Plan4 p = plan(g, a.T, a.max_q, a.hq, a.hkv);
   g.a.hkv = a.hkv * p.split;  // units are counted by parts of a key head's queries
   Begun *begun = reinterpret_cast<Begun *>(a.scratch);
-  g.part_o = reinterpret_cast<float *>(a.scratch + kBegunBytes);
+  g.part_o = reinterpret_cast<float *>(a.scratch + kBegunBytes + kFewBytes);
   if (dtype == MOE_DTYPE_BF16)
     return a.D == 64 ? run_d<MOE_DTYPE_BF16, 64>(g, p, begun, ctas, s)
                      : run_d<MOE_DTYPE_BF16, 128>(g, p, begun, ctas, s);

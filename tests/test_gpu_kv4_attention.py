@@ -346,6 +346,17 @@ def test_a_workspace_serves_every_smaller_call():
     assert torch.equal(got[0], want[0])
 
 
+@pytest.mark.parametrize("byte", [0xFF, 0x7F, 0x01])
+@pytest.mark.parametrize("lens", [[1, 2, 65, 257, 500], [9000], [40] * 300])
+def test_what_a_workspace_held_before_is_nothing(byte, lens):
+    b = Batch(lens, [1] * len(lens), 14, 2, 64, 16, seed=4)
+    o, lse = b.run()
+    b.ws.buf[b.ws.offset + 256:b.ws.offset + b.ws.nbytes] = byte
+    o2, lse2 = b.run()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    b.check(o, lse)
+
+
 def test_cache_past_32_bit_offsets():
     D, page = 128, 256
     kv = moe.kv_struct(8, 1, D, page, 1)
