@@ -17,8 +17,7 @@
 // that is cut into a piece for each warp (attention.cuh): every warp is a worker on
 // its own and streams steps of keys through a private ring in shared memory
 // (cp.async).  A unit that one warp has whole leaves as it should be; of others every
-// warp keeps its part (normalised, with its log-sum-exp), and the joins
-// put those together.
+// warp keeps its part (normalised, with its log-sum-exp), which a second kernel joins.
 //
 // Bound by HBM where contexts are long: 16 sequences of up to 131072 rows (8 key heads
 // of 128, 8 query heads each; 1.30 GB) take 200 us, 0.96 of the measured copy
@@ -612,29 +611,50 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
   __syncwarp();  // before the next stretch's copies
 }
 
+// scan_own by every warp for itself, up to kWarpScan sequences a lane: no barriers, and
+// nothing goes through shared memory.  One token over 1000 rows 10.7 -> 9.5 us, 37
+// sequences of up to 4099 15.3 -> 14.3 (one token of 28 heads of 64 each), 64 of up to 8192
+// 70.9 and 71.0, 128 of up to 1024 32.8 -> 32.9, 256 47.0 -> 49.2.
+constexpr int kWarpScan = 2;
+template <class K>
+__device__ __forceinline__ OwnScan scan_warp(const AttnArgs &g, int per) {
+  const int lane = threadIdx.x & 31;
+  OwnScan r = {};
+  r.b_lo = lane * per;
+  r.b_hi = min(r.b_lo + per, g.a.B);
+  int64_t mine = 0;
+  bool bad_off = false, bad = false;
+#pragma unroll 1
+  for (int b = r.b_lo; b < r.b_hi; ++b) mine += read_seq<K>(g, b, &bad_off, &bad).cost;
+  int64_t cost = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t c = __shfl_up_sync(0xffffffffu, cost, off);
+    if (lane >= off) cost += c;
+  }
+  r.drop = __any_sync(0xffffffffu, bad_off);
+  r.bad = bad || bad_off;
+  r.before = cost - mine;
+  r.total = r.drop ? 0 : __shfl_sync(0xffffffffu, cost, 31);
+  return r;
+}
+
 // Walks the units in [lo, hi) of their line, a whole warp, sequence by sequence from
-// the one where the CTA's scan has lo.  (The walk of attention.cuh looks at 32
+// the one where the scan has lo.  (The walk of attention.cuh looks at 32
 // sequences at a time, which a few units a worker do not pay back: 64 sequences of up
-// to 8192 rows 71.6 us with it, 70.4 so; one
-// token over 1000 rows 11.2 and 10.8.)
+// to 8192 rows 71.6 us with it, 70.4 so; one token over 1000 rows 11.2 and 10.8.)
 template <class K>
 struct Walk4 {
   int64_t lo, hi, start, unit_cost;
   int b, j;
   Seq s;
 
-  template <int THREADS>
-  __device__ __forceinline__ void begin(const AttnArgs &g, const ScanShared<THREADS> &sh,
-                                        int64_t lo_, int64_t hi_) {
+  // from the sequence before `first`, whose units start at `at`
+  __device__ __forceinline__ void begin(int first, int64_t at, int64_t lo_, int64_t hi_) {
     lo = lo_;
     hi = hi_;
-    // the last thread of the scan whose sequences start at or before lo
-    int i = 0;
-    for (int k = threadIdx.x & 31; k < THREADS; k += 32)
-      if (sh.before[k] <= lo) i = k;
-    i = __reduce_max_sync(0xffffffffu, i);
-    b = i * ((g.a.B + THREADS - 1) / THREADS) - 1;
-    start = sh.before[i];
+    b = first - 1;
+    start = at;
     s.cost = 0;
     s.units = j = 0;
     unit_cost = 1;
@@ -717,7 +737,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   if (a.q_offsets) prefetch(a.q_offsets, a.B + 1);
   prefetch(a.page_table, static_cast<int64_t>(a.B) * a.max_pages);
   pdl_begin();
-  const OwnScan own = scan_own<Steps4<NH>>(g, scan);
+  // the line's length, and where this thread's sequences start in it
+  const bool by_warp = a.B <= 32 * kWarpScan;
+  const int per = by_warp ? (a.B + 31) >> 5 : (a.B + WARPS * 32 - 1) / (WARPS * 32);
+  OwnScan own;
+  if (by_warp) {
+    own = scan_warp<Steps4<NH>>(g, per);
+  } else {
+    own = scan_own<Steps4<NH>>(g, scan);
+  }
   if (blockIdx.x == 0 && own.bad) set_status(a.status, kStatusBadId);
   const int64_t workers = gridDim.x * WARPS;
   const int64_t piece = max(quotient(own.total + workers - 1, workers), static_cast<int64_t>(1));
@@ -726,8 +754,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   const int64_t lo = worker * piece, hi = min(lo + piece, own.total);
   Begun goes_on = {0, 0, 0, 0, 0, 0};
   if (lo < hi) {
+    // the last thread of the scan whose sequences start at or before lo
+    int i = 0;
+    int64_t at = 0;
+    if (by_warp) {
+      i = 31 - __clz(__ballot_sync(0xffffffffu, own.before <= lo));
+      at = __shfl_sync(0xffffffffu, own.before, i);
+    } else {
+      for (int k = lane; k < WARPS * 32; k += 32)
+        if (scan.before[k] <= lo) i = k;
+      i = __reduce_max_sync(0xffffffffu, i);
+      at = scan.before[i];
+    }
     Walk4<Steps4<NH>> walk;
-    walk.begin(g, scan, lo, hi);
+    walk.begin(i * per, at, lo, hi);
     Stretch x;
     while (walk.next(g, &x)) {
       float *part = x.s0 > 0 ? part_at<D>(g, worker, kHead)
