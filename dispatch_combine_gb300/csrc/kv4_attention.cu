@@ -862,18 +862,30 @@ __device__ __forceinline__ void write_joined(const AttnArgs &g, const Begun &u, 
     *row.lse = l != 0.0f ? (ref + log2f(l)) * 0.6931471805599453f : isnan(inv) ? inv : -INFINITY;
 }
 
-// The units that several workers had: blockIdx.x is the worker that began one, a warp
-// takes a row.
+// The units that several workers had: a CTA joins those that its workers began, a warp a
+// row (of 8, blockIdx.y says which).  Two workers a CTA: 37 sequences of up to 4099 rows, 6
+// tokens of 7 heads of 64: 24.8 us with one, 24.3 with two, 25.5 with four; 64 of up to 8192
+// (heads of 128) 71.3, 71.2, 72.0.
+constexpr int kJoinWorkers = 2;
 template <int DTYPE, int D>
-__global__ void __launch_bounds__(256, 4) kv4_join_kernel(const AttnArgs g, const Begun *begun) {
+__global__ void __launch_bounds__(256, D == 128 ? 3 : 4) kv4_join_kernel(const AttnArgs g, const Begun *begun) {
   pdl_begin();
-  const int worker = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const Begun u = begun[worker];
-  if (u.parts == 0 || r >= u.ntok * g.G) return;
-  float o[D / 32], l, ref;
-  add_parts<D, 1>(part_at<D>(g, worker, kTail) + r * D, part_at<D>(g, worker, kTail) + g.own.rows * D + r,
-                  2 * part_floats(g.own.rows, D), u.parts, 0, o, &l, &ref);
-  write_joined<DTYPE, D>(g, u, r, o, l, ref);
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  Begun of = {0, 0, 0, 0, 0, 0};
+  if (lane < kJoinWorkers) of = begun[blockIdx.x * kJoinWorkers + lane];
+  unsigned todo = __ballot_sync(0xffffffffu, of.parts != 0 && r < of.ntok * g.G);
+#pragma unroll 1
+  for (; todo; todo &= todo - 1) {
+    const int k = __ffs(todo) - 1;
+    auto take = [&](int v) { return __shfl_sync(0xffffffffu, v, k); };
+    const Begun u = {take(of.parts), take(of.head), take(of.tok0),
+                     take(of.ntok),  take(of.lim0), take(of.kv_len)};
+    const float *tail = part_at<D>(g, blockIdx.x * kJoinWorkers + k, kTail);
+    float o[D / 32], l, ref;
+    add_parts<D, 1>(tail + r * D, tail + g.own.rows * D + r, 2 * part_floats(g.own.rows, D), u.parts, 0,
+                    o, &l, &ref);
+    write_joined<DTYPE, D>(g, u, r, o, l, ref);
+  }
 }
 
 // The same where a batch has few units, which may have many parts each: blockIdx.x is a
@@ -963,7 +975,7 @@ constexpr size_t kFewBytes = (sizeof(int) * kMaxCtas * kMostWarps4 + 255) / 256 
 template <int DTYPE, int D, int NT, int NH, int WARPS>
 cudaError_t run(const AttnArgs &g, int split, Begun *begun, int ctas, cudaStream_t s) {
   using C = Cfg4<D, NH, WARPS>;
-  static_assert(WARPS <= kMostWarps4, "slots of partial results");
+  static_assert(WARPS <= kMostWarps4 && WARPS % 4 == 0, "slots of partial results");
   auto kernel = kv4_attention_kernel<DTYPE, D, NT, NH, WARPS>;
   // once for a device (0.7 us a call)
   static std::atomic<uint64_t> known{0};
@@ -985,8 +997,8 @@ cudaError_t run(const AttnArgs &g, int split, Begun *begun, int ctas, cudaStream
     MOE_LAUNCH_PDL(kv4_join_few_kernel<DTYPE, D>, dim3(static_cast<unsigned>(units), g.own.rows), 256, 0, s,
                    g, begun, few, ctas * WARPS);
   else
-    MOE_LAUNCH_PDL(kv4_join_kernel<DTYPE, D>, dim3(ctas * WARPS, (g.own.rows + 7) / 8), 256, 0, s, g,
-                   begun);
+    MOE_LAUNCH_PDL(kv4_join_kernel<DTYPE, D>, dim3(ctas * WARPS / kJoinWorkers, (g.own.rows + 7) / 8), 256,
+                   0, s, g, begun);
   return cudaGetLastError();
 }
 template <int DTYPE, int D>
