@@ -357,6 +357,28 @@ def test_what_a_workspace_held_before_is_nothing(byte, lens):
     b.check(o, lse)
 
 
+@pytest.mark.parametrize("lens,qs,hq,hkv,D", [
+    ([3000, 0, 1, 2500, 70], [3, 2, 1, 5, 0], 16, 2, 128), ([1900, 2300], [1, 2], 34, 1, 128), ([6000], [7], 28, 4, 64),
+    ([1345, 1400, 64, 65], [1, 1, 1, 1], 64, 16, 64), ([40000], [1], 1, 1, 64),
+])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_few_units_of_many_parts(lens, qs, hq, hkv, D, dtype):
+    b = Batch(lens, qs, hq, hkv, D, 16, dtype, seed=len(lens))
+    o, lse = b.run()
+    b.check(o, lse)
+    # offsets that are refused leave nothing behind for the next call
+    bad = b.offsets.clone()
+    bad[-1] = b.T + 1
+    b.run(q_offsets=bad)
+    assert moe.moe_get_device_status(b.ws) != 0
+    b.ws = moe.Workspace(b.ws.nbytes)
+    o2, lse2 = b.run()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # and a larger batch, whose units are joined in the other way, agrees
+    more = Batch(lens + [1] * 70, qs + [1] * 70, hq, hkv, D, 16, dtype, seed=len(lens))
+    more.check(*more.run())
+
+
 def test_cache_past_32_bit_offsets():
     D, page = 128, 256
     kv = moe.kv_struct(8, 1, D, page, 1)
