@@ -6,7 +6,7 @@
 // are read once, and what is written of keys and values is 9/32 of it.  16384 tokens
 // of 64 + 8 heads of 128 appended and read back (690 MB) take 119 us, 0.86 of the
 // measured copy bandwidth; 131072 rows of 8 heads of 128 read back into a 16-bit
-// cache (689 MB) 117 us, 0.87.  Few rows cost their launch: 64 tokens appended and
+// cache (689 MB, 538 of them written) 117 us, 0.87.  Few rows cost their launch: 64 tokens appended and
 // read back 5.2 us.
 //   What the append was bound by first was arithmetic: with sines in 64 bits and
 // divisions as they are written (119 us now) it was 216, with either of the two

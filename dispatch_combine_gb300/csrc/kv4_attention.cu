@@ -21,11 +21,11 @@
 //
 // Bound by HBM where contexts are long: 16 sequences of up to 131072 rows (8 key heads
 // of 128, 8 query heads each; 1.30 GB) take 200 us, 0.96 of the measured copy
-// bandwidth; without the arithmetic 198.  64 of up to 8192 (364 MB) take 71, 17 of them
-// outside the stream: the two launches and the scan 5, pages and first rows 3, the
-// last rows' way and the join.  Several queries of a sequence are bound by the
+// bandwidth; without the arithmetic 198.  64 of up to 8192 (364 MB) take 71: 2.5 until the
+// first rows are asked for, 57 while they stream (0.93), 4 in which workers end one after
+// the other, 7 for the join.  Several queries of a sequence are bound by the
 // arithmetic (510 instructions for 32 keys x 8 rows of 128): 37 sequences of up to
-// 4099, 6 tokens of 7 heads of 64 each (20 MB) 25 us.
+// 4099, 6 tokens of 7 heads of 64 each (20 MB) 24 us.
 //   Other ways, each measured against this one as it then was (64 sequences, or 16
 // where it says so): the offset of the values by one more product instead of a
 // subtraction 81 -> 85 us; 16 warps (128 registers, spills) 73 -> 83, 10 or 11 warps
