@@ -6,7 +6,7 @@
 //   token = min { v : sum_{w <= v} r_w > u sum r }.
 // One row of p and one of q are read for each sequence, by a cluster of CTAs: 64
 // sequences of 7 drafts over 131072 tokens in fp32 (67 MB) take 16 us, 0.62 of the
-// measured copy bandwidth; one sequence over 32000 5.1.  What bounds it is the chain
+// measured copy bandwidth; one sequence over 32000 4.9.  What bounds it is the chain
 // of dependent reads: offsets, drafts, their probabilities, the row, the sums of the
 // cluster's CTAs, and the border's piece once more (from L2).
 //
@@ -131,6 +131,11 @@ template <int DTYPE>
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a, const int ctas) {
   pdl_begin();
   __shared__ uint64_t s_sums[kWarps];
+  struct Found {
+    uint64_t total, border, before;
+    int owner;
+  };
+  __shared__ Found s_found;
   const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q0 = a.offsets[b], q1 = a.offsets[b + 1];
@@ -144,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
     return;
   }
   const int n = q1 - q0 - 1;
+  const float last = a.uniforms[q1 - 1];  // asked for now, needed late (one sequence 5.2 -> 4.9 us)
   const int size = DTYPE == MOE_DTYPE_FP32 ? 4 : 2;
   // ---- the drafts before the first that falls; every warp for itself
   int accepted = n, fallen = -1;
@@ -222,22 +228,19 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
     own = warp_sum(own);
     if (lane == 0) s_sums[warp] = own;
     cluster_sync_all();
-    // every warp: lane k has parts k and k + 32
-    uint64_t sum[2] = {0, 0};
+    // The first warp looks for the border's part for all of them (each for itself takes
+    // issue slots from the other CTAs: 37 sequences over 50021 tokens 7.4 us, so 7.1):
+    // lane k has parts k and k + 32.
+    if (warp == 0) {
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = lane + 32 * i;
-      if (k < parts) {
-        const uint32_t at = mapa_shared(&s_sums[k % kWarps], k / kWarps);
-        asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(sum[i]) : "r"(at) : "memory");
+      for (int i = 0; i < 2; ++i) {
+        const int k = lane + 32 * i;
+        if (k < parts) {
+          const uint32_t at = mapa_shared(&s_sums[k % kWarps], k / kWarps);
+          asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(sum[i]) : "r"(at) : "memory");
+        }
       }
-    }
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the sums have been read
-    const uint64_t first = warp_sum(sum[0]);
-    total = first + warp_sum(sum[1]);
-    if (total > 0) {
-      border = part_of(a.uniforms[q1 - 1], total);
       uint64_t cum[2] = {sum[0], sum[1]};
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1)
@@ -246,13 +249,24 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
           const uint64_t up = __shfl_up_sync(0xffffffffu, cum[i], off);
           if (lane >= off) cum[i] += up;
         }
+      const uint64_t first = __shfl_sync(0xffffffffu, cum[0], 31);
+      total = first + __shfl_sync(0xffffffffu, cum[1], 31);
+      border = part_of(last, total);
       const unsigned past = __ballot_sync(0xffffffffu, cum[0] > border);
       const unsigned late = __ballot_sync(0xffffffffu, cum[1] + first > border);
-      owner = past ? __ffs(past) - 1 : 31 + __ffs(late);
+      owner = past ? __ffs(past) - 1 : 31 + __ffs(late);  // total 0: it is not looked at
       const uint64_t upto = past ? cum[0] - sum[0] : cum[1] - sum[1] + first;
       before = __shfl_sync(0xffffffffu, upto, owner & 31);
-      break;
+      if (lane == 0) s_found = {total, border, before, total > 0 ? owner : -1};
     }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the sums have been read
+    __syncthreads();
+    total = s_found.total;
+    border = s_found.border;
+    before = s_found.before;
+    owner = s_found.owner;
+    if (total > 0) break;
     if (again) break;
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     r.q = nullptr;  // nothing is left of the difference: the target's own row
