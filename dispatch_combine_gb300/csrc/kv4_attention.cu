@@ -612,20 +612,26 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
 }
 
 // scan_own by every warp for itself, up to kWarpScan sequences a lane: no barriers, and
-// nothing goes through shared memory.  One token over 1000 rows 10.7 -> 9.5 us, 37
+// nothing goes through shared memory; `gaps`: there may be tokens that no unit has.  One token over 1000 rows 10.7 -> 9.5 us, 37
 // sequences of up to 4099 15.3 -> 14.3 (one token of 28 heads of 64 each), 64 of up to 8192
 // 70.9 and 71.0, 128 of up to 1024 32.8 -> 32.9, 256 47.0 -> 49.2.
 constexpr int kWarpScan = 2;
 template <class K>
-__device__ __forceinline__ OwnScan scan_warp(const AttnArgs &g, int per) {
+__device__ __forceinline__ OwnScan scan_warp(const AttnArgs &g, int per, bool *gaps) {
   const int lane = threadIdx.x & 31;
   OwnScan r = {};
   r.b_lo = lane * per;
   r.b_hi = min(r.b_lo + per, g.a.B);
   int64_t mine = 0;
-  bool bad_off = false, bad = false;
+  bool bad_off = false, bad = false, gap = false;
 #pragma unroll 1
-  for (int b = r.b_lo; b < r.b_hi; ++b) mine += read_seq<K>(g, b, &bad_off, &bad).cost;
+  for (int b = r.b_lo; b < r.b_hi; ++b) {
+    const Seq s = read_seq<K>(g, b, &bad_off, &bad);
+    mine += s.cost;
+    gap |= s.nq > 0 && s.steps == 0;
+    gap |= (b == 0 && s.q0 > 0) || (b == g.a.B - 1 && s.q0 + s.nq < g.a.T);
+  }
+  *gaps = __any_sync(0xffffffffu, gap) || g.a.B == 0;
   int64_t cost = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -741,8 +747,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   const bool by_warp = a.B <= 32 * kWarpScan;
   const int per = by_warp ? (a.B + 31) >> 5 : (a.B + WARPS * 32 - 1) / (WARPS * 32);
   OwnScan own;
+  bool gaps = true;
   if (by_warp) {
-    own = scan_warp<Steps4<NH>>(g, per);
+    own = scan_warp<Steps4<NH>>(g, per, &gaps);
   } else {
     own = scan_own<Steps4<NH>>(g, scan);
   }
@@ -783,7 +790,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     begun[worker] = goes_on;
     if (few) few[worker] = short_form(a, goes_on);
   }
-  if (own.drop) return;
+  if (own.drop || !gaps) return;
   bool p = false, q = false;
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const Seq s = read_seq<Steps4<NH>>(g, b, &p, &q);
