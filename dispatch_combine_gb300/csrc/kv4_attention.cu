@@ -25,7 +25,7 @@
 // first rows are asked for, 57 while they stream (0.93), 4 in which workers end one after
 // the other, 7 for the join.  Several queries of a sequence are bound by the
 // arithmetic (510 instructions for 32 keys x 8 rows of 128): 37 sequences of up to
-// 4099, 6 tokens of 7 heads of 64 each (20 MB) 24 us.
+// 4099, 6 tokens of 7 heads of 64 each (20 MB) 23.6 us.
 //   Other ways, each measured against this one as it then was (64 sequences, or 16
 // where it says so): the offset of the values by one more product instead of a
 // subtraction 81 -> 85 us; 16 warps (128 registers, spills) 73 -> 83, 10 or 11 warps
@@ -83,7 +83,10 @@ struct Cfg4 {
   static constexpr int CODES = KEYS * CB;  // bytes of a step's keys or values
   static constexpr int SCALES = KEYS * SB;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // key codes, values', key scales, values'
-  static constexpr int STAGES = std::min(8, std::max(2, 170 * 1024 / (WARPS * STAGE)));
+  // One step on its way while one is read: the SM's other warps fill the rest.  37 sequences
+  // of up to 4099, 6 tokens of 7 heads of 64: 23.7 us, three 24.3, four 24.5; 64 of up to
+  // 8192, 2 tokens of 8 heads of 128: 80.1, 81.7, 82.7.
+  static constexpr int STAGES = 2;
   static constexpr int WARP_BYTES = STAGES * STAGE;
   static constexpr int SMEM_BYTES = WARPS * WARP_BYTES;
 };
@@ -213,7 +216,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
   const int rows = x.ntok * g.G;
   // row r is head r % G of token r / G (exact for the few rows there are)
   auto token_of = [&](int r) { return r * g.tpt >> 16; };
-  // ---- the ring.  A step is two runs of 16 rows, each in one page; lane i keeps
+  // ---- the ring.  A step is NH runs of 16 rows, each in one page; lane i keeps
   // the page of run `page0 + i`.
   const int kvh = x.head / split, heads = a.hkv / split;
   const int spp = a.page_shift - 4;  // log2 of runs per page
@@ -578,6 +581,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
   // ---- the rows leave through the ring, where they come to lie in order (and the
   // accumulators' registers are free for the stores)
   float *held = reinterpret_cast<float *>(space);
+  static_assert(8 * NT * (D + 1) * sizeof(float) <= C::WARP_BYTES, "rows and their sums in the ring");
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float2 sums = unpack_f32x2(l[nt]), offs = unpack_f32x2(c0[nt]);
