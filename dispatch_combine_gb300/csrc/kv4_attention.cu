@@ -245,7 +245,7 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
   auto load = [&](int s) {  // past the end: an empty group
     if (s < x.s1) {
       const int run = NH * s, mask = (1 << spp) - 1;
-      if (run - page0 >= 32) fetch_pages(run);
+      if (run + NH - page0 > 32) fetch_pages(run);
       const uint32_t dst = into + lane * 16;
 #pragma unroll
       for (int j = 0; j < NH; ++j) {
