@@ -379,6 +379,27 @@ def test_few_units_of_many_parts(lens, qs, hq, hkv, D, dtype):
     more.check(*more.run())
 
 
+@pytest.mark.parametrize("hq,hkv,D", [(8, 1, 128), (14, 2, 64)])
+def test_a_graph_follows_the_lengths(hq, hkv, D):
+    """Few units in many parts, in one, in none: what a call left in the workspace is nothing to the next."""
+    b = Batch([4000, 2000], [1, 1], hq, hkv, D, 16, seed=2)
+    full = b.kv_lens.clone()
+    b.run()
+    out = torch.full((2, hq, D), 9.0, dtype=BF16, device="cuda")
+    lse = torch.full((2, hq), 9.0, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.run(out=out, lse=lse)
+    for lens in ([4000, 2000], [1, 1], [0, 2000], [3999, 64], [65, 0], [0, 0], [4000, 2000]):
+        b.kv_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        k, v, n = b.k, b.v, b.lens
+        b.k, b.v, b.lens = [x[:m] for x, m in zip(k, lens)], [x[:m] for x, m in zip(v, lens)], lens
+        b.check(out, lse)
+        b.k, b.v, b.lens = k, v, n
+    assert torch.equal(b.kv_lens, full)
+
+
 def test_cache_past_32_bit_offsets():
     D, page = 128, 256
     kv = moe.kv_struct(8, 1, D, page, 1)
