@@ -635,6 +635,10 @@ __device__ __forceinline__ OwnScan scan_warp(const AttnArgs &g, int per, bool *g
     gap |= s.nq > 0 && s.steps == 0;
     gap |= (b == 0 && s.q0 > 0) || (b == g.a.B - 1 && s.q0 + s.nq < g.a.T);
   }
+  if (g.a.B == 0) {  // no sequence reads the one offset that there is
+    const int q0 = g.a.q_offsets[0];
+    bad_off = q0 < 0 || q0 > g.a.T;
+  }
   *gaps = __any_sync(0xffffffffu, gap) || g.a.B == 0;
   int64_t cost = mine;
 #pragma unroll
@@ -794,7 +798,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     begun[worker] = goes_on;
     if (few) few[worker] = short_form(a, goes_on);
   }
-  if (own.drop || !gaps) return;
+  if (own.drop || !gaps) return;  // offsets within [0, T] from here on
   bool p = false, q = false;
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const Seq s = read_seq<Steps4<NH>>(g, b, &p, &q);
