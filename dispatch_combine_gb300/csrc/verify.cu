@@ -161,8 +161,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
       x = a.tokens[q0 + i + 1];
       const int64_t row = q0 + i;
       if (x < 0 || x >= a.vocab) {
-        if (writer) set_status(a.status, kStatusBadId);
-        falls = true;
+        falls = true;  // and is reported below, with those that are not looked at here
       } else {
         const double p = prob_at<DTYPE>(a.target, row * a.target_stride + x);
         const double q = a.draft ? prob_at<DTYPE>(a.draft, row * a.draft_stride + x) : 1.0f;
@@ -349,7 +348,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
   }
   if (rank == 0) {
     for (int i = threadIdx.x; i <= n; i += kThreads) {
-      if (i < accepted) a.out_tokens[q0 + i] = a.tokens[q0 + i + 1];
+      if (i < n) {
+        const int x = a.tokens[q0 + i + 1];
+        if (x < 0 || x >= a.vocab) set_status(a.status, kStatusBadId);
+        if (i < accepted) a.out_tokens[q0 + i] = x;
+      }
       if (i > accepted) a.out_tokens[q0 + i] = -1;
     }
     if (threadIdx.x == 0) {
