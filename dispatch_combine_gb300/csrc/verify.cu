@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
     if (a.draft) {
       r.q = static_cast<const uint8_t *>(a.draft) + row * a.draft_stride * size;
       alike = ((reinterpret_cast<uintptr_t>(r.p) ^ reinterpret_cast<uintptr_t>(r.q)) & 15) == 0;
-    } else {
+    } else if (fallen >= 0 && fallen < a.vocab) {
       r.without = fallen;
     }
   }
