@@ -854,8 +854,9 @@ __device__ __forceinline__ void add_parts(const float *parts, const float *lses,
     for (int c = 0; c < kBatch; ++c) {
       const float w = __shfl_sync(0xffffffffu, weight, (k + c) & 31);
       l += w;
+      if (k + c < count)  // a part that weighs nothing, too: it may be NaN
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = w == 0.0f ? o[e] : fmaf(w, x[c][e], o[e]);
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[c][e], o[e]);
     }
     if (k + kBatch < count) fetch(k + kBatch);
   }
@@ -957,7 +958,6 @@ __global__ void __launch_bounds__(256) kv4_join_few_kernel(const AttnArgs g, con
 #pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     const float weight = ex2(s_ref[w] - ref);
-    if (weight == 0.0f) continue;
     l = fmaf(weight, s_l[w], l);
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fmaf(weight, s_o[w][lane * E + e], o[e]);
