@@ -68,12 +68,23 @@ struct Steps4 {
 
 constexpr int kMostWarps4 = 12;  // of a CTA
 
-// Probabilities are 2^(score + c0), c0 = kOff - ev - max, where the value scales
-// are below 2^(ev + 1): 2^(kOff + kLag) at most, and with a scale below 2^15.5.
+// Probabilities are 2^(score + c0), c0 = kOff - max: 2^(kOff + kLag) at most, and twice
+// that with a value scale, which is taken times a power of two that puts it below 2.
 // Past kMost the rounding of c0 could carry them out of fp16; such rows are NaN.
 struct Prob4 {
   static constexpr float kOff = 9.0f, kLag = 5.0f, kMost = 16777216.0f;
 };
+// Each group's value scales are taken times a power of two of their own, which puts the
+// largest that a warp meets at a unit's first step below 1 and moves when a larger one
+// would be 2 or more.  So what fp16 loses of a product of probability and scale is
+// measured by the group's own values: 2^-33 of the largest probability times that scale, and
+// 2^-24 of that scale.  Scales below kLeastScale4 count as that.  (From 1 to 2 at the first
+// step most units would meet a larger one later: 64 sequences of up to 8192 rows, 128 + 8
+// heads of 128, 102.4 us so, 105.5 with it.)
+//   One power of two for all values, and never below 1, lost small values beside a key that
+// took the weight: 100.7 us there, with 64 + 8 heads of 128 in fp16 72.5 (75.6 now), others
+// within 1 %.
+constexpr float kLeastScale4 = 1.0f / 65536.0f;
 
 template <int D, int NH, int WARPS>
 struct Cfg4 {
@@ -113,6 +124,15 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&v)[N]) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr));
   else
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr));
+}
+template <int N>
+__device__ __forceinline__ void sts(uint32_t addr, const uint32_t (&v)[N]) {
+  if constexpr (N == 4)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3])
+                 : "memory");
+  else
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v[0]), "r"(v[1]) : "memory");
 }
 __device__ __forceinline__ void sts_zero16(uint32_t addr) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(0)) : "memory");
@@ -345,7 +365,9 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
 
   float o[NT][NB][2][4];
   uint64_t c0[NT], l[NT];
-  float ev = 0.0f;
+  uint32_t lift[NB];  // the power of two of each group's value scales, twice
+#pragma unroll
+  for (int b = 0; b < NB; ++b) lift[b] = 0x78007800u;  // 2^15, the most
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -437,10 +459,9 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
       const unsigned evens = __ballot_sync(0xffffffffu, even), odds = __ballot_sync(0xffffffffu, odd);
       if (evens | odds) {
         const uint32_t keep = (even ? 0u : 0xFFFFu) | (odd ? 0u : 0xFFFF0000u);
-        if (lane < 8 * NH)
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * b), "r"(w[b] & keep) : "memory");
+        for (int b = 0; b < NB; ++b) w[b] &= keep;
+        if (lane < 8 * NH) sts<NB>(at, w);
         __syncwarp();
         const unsigned mine = (gr & 1 ? odds : evens) >> (gr >> 1);
 #pragma unroll
@@ -454,8 +475,8 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
       }
     }
     // ---- exponents.  The running maximum moves when a score passes it by the lag,
-    // and the exponent of the value scales when one passes it (the test is of the
-    // top bit of fp16 exponents: 2 or more).
+    // and a group's power of two when a scale times it is 2 or more (the top bit of an
+    // fp16 exponent; NaN, too).
     uint64_t ex[NH][NT][2];
     float most = -INFINITY;
     auto exponents = [&]() {
@@ -472,21 +493,27 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
           }
     };
     exponents();
-    uint32_t any[NB];
-    lds<NB>(ss + C::SCALES + lane % (8 * NH) * (2 * C::SB), any);
-    uint32_t two = any[0];
+    uint32_t any[NB], lifted[NB], two = 0;
+    const uint32_t any_at = ss + C::SCALES + lane % (8 * NH) * (2 * C::SB);
+    lds<NB>(any_at, any);
 #pragma unroll
-    for (int b = 1; b < NB; ++b) two |= any[b];
-    if (__any_sync(0xffffffffu, most > Prob4::kOff + Prob4::kLag - ev || (two & 0x40004000u) ||
-                                    s == x.s0)) {
-      float big = 0.0f;
+    for (int b = 0; b < NB; ++b) {
+      lifted[b] = hmul2(any[b], lift[b]);
+      two |= lifted[b];
+    }
+    if (__any_sync(0xffffffffu, most > Prob4::kOff + Prob4::kLag || (two & 0x40004000u) || s == x.s0)) {
+      float to[NB];  // of the accumulators, by groups
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float2 p = half2_at(any[b]);
-        big = fmaxf(big, fmaxf(p.x, p.y));
+        const float big = fmaxf(fmaxf(p.x, p.y), kLeastScale4);  // NaN is none
+        const uint32_t top_s = __reduce_max_sync(0xffffffffu, __float_as_uint(big)) & 0x7F800000u;
+        const float was = half2_at(lift[b]).x;
+        const float is = fminf(was, __uint_as_float((253u << 23) - top_s));  // 1 / (2 top_s)
+        to[b] = is * __uint_as_float((254u << 23) - __float_as_uint(was));
+        lift[b] = pack_f16x2(is, is);
+        lifted[b] = hmul2(any[b], lift[b]);
       }
-      const unsigned top_s = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-      const float ev1 = fmaxf(ev, static_cast<float>(static_cast<int>(top_s >> 23) - 127));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 m = unpack_f32x2(sl2[nt]), was = unpack_f32x2(c0[nt]);
@@ -502,9 +529,9 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           const float u = c ? m.y : m.x, old = c ? was.y : was.x;
           // each column by its own scores, so that no head's bits depend on another's
-          is[c] = old + (ev - ev1);
-          if (s == x.s0 || fmaf(top, u, old) > Prob4::kOff + Prob4::kLag - ev)
-            is[c] = fmaf(-fmaxf(top, fmaxf(-Prob4::kMost / u, -FLT_MAX)), u, Prob4::kOff - ev1);
+          is[c] = old;
+          if (s == x.s0 || fmaf(top, u, old) > Prob4::kOff + Prob4::kLag)
+            is[c] = fmaf(-fmaxf(top, fmaxf(-Prob4::kMost / u, -FLT_MAX)), u, Prob4::kOff);
           f[c] = ex2(is[c] - old);
           if (s == x.s0) f[c] = 0.0f;
         }
@@ -514,13 +541,15 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            o[nt][b][0][e] *= f[e & 1];
-            o[nt][b][1][e] *= f[e & 1];
+            o[nt][b][0][e] *= f[e & 1] * to[b];
+            o[nt][b][1][e] *= f[e & 1] * to[b];
           }
       }
-      ev = ev1;
       exponents();
     }
+    // the scales as they are used (every lane has read its own: the vote needed them)
+    if (lane < 8 * NH) sts<NB>(any_at, lifted);
+    __syncwarp();
     // ---- probabilities, as the second operand: keys along the contraction
 #pragma unroll
     for (int half = 0; half < NH; ++half) {
@@ -597,13 +626,15 @@ __device__ __forceinline__ void attend(const AttnArgs &g, const Stretch &x, int 
       if (off < -Prob4::kMost) sum = NAN;
       const float lse = sum == 0.0f ? -INFINITY : log2f(sum) - off;
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const float low = inv * 16777216.0f, high = inv * 1048576.0f;
       float *row = held + r * D + 4 * gr;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) {
+        const float down = __uint_as_float((254u << 23) - __float_as_uint(half2_at(lift[b]).x));
+        const float low = inv * 16777216.0f * down, high = inv * 1048576.0f * down;
         *reinterpret_cast<float4 *>(row + 32 * b) =
             make_float4(o[nt][b][0][c] * low, o[nt][b][0][2 + c] * high, o[nt][b][1][c] * low,
                         o[nt][b][1][2 + c] * high);
+      }
       if (gr == 0) held[8 * NT * D + r] = lse;
     }
   }

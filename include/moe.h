@@ -689,8 +689,12 @@ moe_status_t moe_kv4_read(const moe_kv_t *kv, int32_t n, const int32_t *slots,
  *   held in fp16 after each row's power of two is taken out (elements below 2^-28
  *   of the row's largest, or below 2^-36, lose bits); the products of the
  *   probabilities with the value scales are rounded to fp16, for bf16 the
- *   probabilities before them too.  A head whose query passes 2^115, or holds a NaN
- *   or an infinity, or whose largest score passes 1.1e7 in magnitude, gets NaN.
+ *   probabilities before them too.  These are held by the largest probability p and,
+ *   for each group of 32 elements, its largest value scale S (2^-16 at least): a key
+ *   below about 2^-22 p loses bits, what it adds is off by no more than 7 * 2^-33 p S and
+ *   2^-34 p of its value, and each value by no more than 7 * 2^-24 S.
+ *   A head whose query passes 2^115, or holds a NaN or an infinity, or whose largest
+ *   score passes 1.1e7 in magnitude, gets NaN.
  * A row that stands for NaN makes NaN of the query heads that see it (at least of
  * the elements of its group, where only its value does) and is nothing to others;
  * what lies past kv_lens is never used.
