@@ -977,10 +977,12 @@ def _one_device():
 
 
 def _here(*tensors):
-    """The tensors of a call are on the current device, whose stream it runs on."""
+    """The tensors of a call and its workspace are on the current device, whose stream it
+    runs on."""
     if _one_device():
         return
     for t in tensors:
+        t = getattr(t, "buf", t)  # a workspace's memory
         if t is not None and t.is_cuda and t.get_device() != _current_device():
             raise ValueError(f"tensor on cuda:{t.get_device()}, not on the current device")
 
@@ -1002,7 +1004,7 @@ def moe_kv4_append(kv: MoeKv, q, k, v, positions, slots, inv_freq, k_cache, v_ca
                    ws: Workspace = None, style=MOE_ROPE_HALF, q_out=None, stream=None):
     """moe_kv_append to a 4-bit cache (see moe_kv4_append in moe.h): k and v are
     quantised in groups of 32 elements as they are written."""
-    _here(k, v, q, k_cache, v_cache)
+    _here(k, v, q, positions, slots, inv_freq, k_cache, v_cache, ws, q_out)
     return _append("moe_kv4_append", kv, torch.uint8, _kv4_cache(kv), q, k, v, positions, slots,
                    inv_freq, k_cache, v_cache, ws, style, q_out, stream)
 
@@ -1015,7 +1017,7 @@ def moe_kv4_read(kv: MoeKv, slots, k_cache, v_cache, ws: Workspace = None, k_out
     slot of -1 leaves its row as it was (zeros, where the outputs are made here)."""
     dt = _kv_dtype(kv)
     n, hkv, D = slots.shape[0], kv.num_kv_heads, kv.head_dim
-    _here(slots, k_cache, v_cache, k_out, v_out, dst_slots)
+    _here(slots, k_cache, v_cache, ws, k_out, v_out, dst_slots)
     cache = _kv4_cache(kv)
     dst, pages, ks, vs = None, 0, 0, 0
     if dst_slots is not None:
@@ -1059,7 +1061,7 @@ def moe_kv4_attention(kv: MoeKv, q, k_cache, v_cache, page_table, kv_lens, ws: W
     or None)."""
     dt = _kv_dtype(kv)
     T, B, hq = q.shape[0], kv_lens.shape[0], kv.num_q_heads
-    _here(q, k_cache, v_cache, page_table, kv_lens, q_offsets, out, lse)
+    _here(q, k_cache, v_cache, page_table, kv_lens, ws, q_offsets, out, lse)
     shape = (T, hq, kv.head_dim)
     qp, qs = _heads(q, dt, shape, "q")
     if out is None:
@@ -1103,7 +1105,7 @@ def moe_verify_drafts(target, tokens, uniforms, offsets, draft=None, ws: Workspa
     B = offsets.shape[0] - 1
     if dt not in _PROB_DTYPES:
         raise TypeError(f"target: expected torch.float32, bfloat16 or float16, got {dt}")
-    _here(target, tokens, uniforms, offsets, draft, accepted, out_tokens)
+    _here(target, tokens, uniforms, offsets, draft, ws, accepted, out_tokens)
     tp, ts = _rows(target, dt, shape, "target")
     dp, ds = (None, 0) if draft is None else _rows(draft, dt, shape, "draft")
     if accepted is None:
