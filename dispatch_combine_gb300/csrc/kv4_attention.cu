@@ -9,7 +9,8 @@
 // up n 2^-20, so decoding is one AND per two elements, and the powers of two come
 // off the scale of the scores and of the output.  The offset of 8 comes off the
 // scores in one product of the key's scales with -8 sum q, and off the values' numbers
-// before theirs (exact).  Nothing of the cache is rounded on the way.
+// before theirs (exact).  Nothing of the cache is rounded on the way but value scales far
+// below the largest of their group (kLeastScale4).
 //
 // Keys are the rows (M = 16) of the instruction and query rows its columns (N =
 // 8), so that 8 query heads of a key head, the usual number, fill it.  Units are a
@@ -24,8 +25,10 @@
 // bandwidth; without the arithmetic 198.  64 of up to 8192 (364 MB) take 71: 2.5 until the
 // first rows are asked for, 57 while they stream (0.93), 4 in which workers end one after
 // the other, 7 for the join.  Several queries of a sequence are bound by the
-// arithmetic (510 instructions for 32 keys x 8 rows of 128): 37 sequences of up to
-// 4099, 6 tokens of 7 heads of 64 each (20 MB) 23.6 us.
+// arithmetic (520 instructions for 32 keys x 8 rows of 128): 37 sequences of up to
+// 4099, 6 tokens of 7 heads of 64 each (20 MB) 23.7 us.  A unit has 16 rows: 64 sequences
+// of up to 8192 rows, 64 + 8 heads of 128, take 81 us with 2 tokens each and 195 with 8, and
+// 103 with one token of 128 heads.
 //   Other ways, each measured against this one as it then was (64 sequences, or 16
 // where it says so): the offset of the values by one more product instead of a
 // subtraction 81 -> 85 us; 16 warps (128 registers, spills) 73 -> 83, 10 or 11 warps
@@ -34,7 +37,8 @@
 // on one SM, joined in shared memory 72 -> 84.
 //
 // Rounded to fewer bits: queries to fp16 after taking out each row's power of two
-// (its largest element is put at 2^14: bf16 ones lose nothing above 2^-28 of it);
+// (its largest element is put at 2^14 to 2^15, elements at odd places 2^4 lower than
+// others: those above 2^-24 of the largest, with bf16 2^-27, keep all their bits);
 // probabilities times the value scales to fp16 for the product with V (the tensor
 // cores take 16-bit operands).  Where the output is bf16, whose own rounding is
 // eight times coarser, the probabilities are rounded first and multiplied two at a
@@ -57,8 +61,9 @@ namespace {
 // sequences of up to 131072 rows took 215 us with 32 keys, 202 with 64; 37 sequences,
 // 6 tokens of 7 heads of 64: 28.7 with 32 keys and 12 warps, 28.4 with 64 and 12, 25.2
 // with 64 and 8 (fewer parts to join).  Two blocks of query rows of 128 leave no
-// registers for 64.  A unit costs its start besides: 64 sequences of 8192 rows, 16
-// query heads each: 112 us counting 2 steps of 32 for it, 105 counting 4.
+// registers for 64.  A unit costs its start besides: 64 sequences of up to 8192 rows, 16
+// query heads to each of 8 key heads: 112 us counting 2 steps of 32 for it, 105 counting 4
+// (102.8 as it is now).
 template <int NH>
 struct Steps4 {
   static constexpr int kKeys = 16 * NH, kUnitCost = NH == 4 ? 2 : 4;

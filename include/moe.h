@@ -685,9 +685,11 @@ moe_status_t moe_kv4_read(const moe_kv_t *kv, int32_t n, const int32_t *slots,
  * the page table.  A long prefix shared by many sequences, or a long chunk of new
  * tokens, is better read back into a 16-bit cache (moe_kv4_read) for
  * moe_prefix_attention.
- *   The cache's numbers and scales enter the products unrounded; queries are
- *   held in fp16 after each row's power of two is taken out (elements below 2^-28
- *   of the row's largest, or below 2^-36, lose bits); the products of the
+ *   The cache's numbers and scales enter the products unrounded, but for value scales
+ *   below 2^-13 of their group's largest; queries are
+ *   held in fp16 after each row's power of two is taken out (elements below 2^-24 of
+ *   the row's largest lose bits, bf16 ones those below 2^-27 of it or below 2^-37; by no
+ *   more than 2^-35 of the largest, or 2^-45); the products of the
  *   probabilities with the value scales are rounded to fp16, for bf16 the
  *   probabilities before them too.  These are held by the largest probability p and,
  *   for each group of 32 elements, its largest value scale S (2^-16 at least): a key
@@ -737,6 +739,8 @@ moe_status_t moe_kv4_attention(const moe_kv_t *kv, int32_t T, int32_t num_seqs, 
  * status word (ws of at least 256 bytes; NULL: not reported), as are offsets that
  * decrease or leave [0, T], whose sequences get accepted = 0 and no tokens.  A
  * sequence without rows gets accepted = 0.
+ * Rows of target and draft may start anywhere, but those that start alike modulo 16
+ * bytes are read in up to half the time (same strides, or both multiples of 16 bytes).
  * vocab from 1 to 2^30; num_seqs <= 2^27 (MOE_ERR_UNSUPPORTED beyond).
  */
 moe_status_t moe_verify_drafts(int32_t T, int32_t num_seqs, int32_t vocab, int32_t dtype,
